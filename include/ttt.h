@@ -60,6 +60,10 @@ extern "C" {
 /* ttt_linear_forward_rope only: rotate the feature pairs (k, k + d/2) (the half-split rotation
  * applied directly, without permute_qk / undo_permute_qk) instead of (2k, 2k+1). */
 #define TTT_FLAG_ROPE_HALF_SPLIT 4u
+/* ttt_selective_scan_*: delta passes through softplus after its bias. */
+#define TTT_FLAG_SOFTPLUS 8u
+/* ttt_causal_conv_*: the output passes through silu. */
+#define TTT_FLAG_SILU 16u
 
 /* Bits of the device status word */
 #define TTT_STATUS_TIMEOUT 1u /* a kernel gave up on a bounded wait and returned early */
@@ -512,6 +516,198 @@ int ttt_linear_backward_ckpt(const void* XQ, const void* XK, const void* XV, con
                              const float* dW_last, const float* db_last, void* dXQ, void* dXK, void* dXV,
                              float* d_lr, float* dW0, float* db0, float* d_ln_w, float* d_ln_b, void* workspace,
                              long long workspace_bytes, void* stream);
+
+/* ---- sequence mixers beside the TTT scan: short causal convolution and selective scan ---------
+ * A layer of this family (the "Mamba" backbone that the walkthrough's apply_gate belongs to) runs a
+ * short causal convolution over the tokens and then a selective state space scan, whose state, like
+ * TTT's, is of fixed size per sequence.  Both come for prompts, for single tokens and with their
+ * gradients.  (No counterpart on the pages.)
+ *
+ * Shared conventions:
+ *  - Activations are rows of channels: a dense batch [n_seq, L, dim], or, with cu_seqlens, packed
+ *    sequences [L, dim] of which sequence b owns the rows cu_seqlens[b] .. cu_seqlens[b+1] - 1
+ *    (int32 [n_seq + 1] on the device, not decreasing, within [0, L]; entries outside [0, L] are held
+ *    inside it, so a bad array cannot make a call read or write out of bounds).  Rows past the last
+ *    sequence are neither read nor written.  Sequences may be empty, L may be 0.
+ *  - strides: NULL for contiguous rows, or a HOST array of element strides, (batch, token) for each
+ *    operand in the order that the call names; channels are contiguous.  Input strides may be 0 (a
+ *    broadcast row); an output's rows must not overlap.  With cu_seqlens the batch strides are not
+ *    used.  Rows need no alignment beyond their element's; 16-byte aligned rows are read faster.
+ *  - States lie in pages of a pool, page p of [n_pages, ...] at p; sequence b uses page pages[b]
+ *    (int32 [n_seq] on the device), or page b if pages is NULL.  A sequence whose entry is negative or
+ *    >= n_pages has no state: prompts start from zeros and keep nothing, steps leave its row of out as
+ *    it was.  The pages of one call have to differ from each other: if two sequences name one page,
+ *    that page and the two sequences' results are unspecified (nothing else is touched).
+ *  - dtype is that of the activations and of the convolution's state; weights, biases, A, D and the
+ *    scan's state are float32.  Sums, states and the gradients of the parameters are held in float32;
+ *    results are rounded to dtype once.
+ *  - The calls allocate nothing, wait for nothing on the device and may be captured into a graph.
+ *    Results do not depend on timing.  Sizes: n_seq <= 2^24, L < 2^30, dim <= 2^24.
+ */
+
+/*
+ * ttt_causal_conv_forward -- out[t][d] = act(bias[d] + sum_w weight[d][w] x[t - (width-1) + w][d]).
+ *   x            [n_seq, L, dim] dtype (or packed).  May be NULL only when L == 0.
+ *   weight       [dim, width] float32, width 2, 3 or 4;  bias [dim] float32 or NULL.
+ *   strides      x, out.
+ *   state_in     pool [n_pages, width-1, dim] dtype or NULL: the width - 1 inputs before each
+ *                sequence's first (oldest first); zeros if NULL.
+ *   state_out    the same pool shape or NULL: receives the last width - 1 inputs (for the next part
+ *                of the sequence or ttt_causal_conv_step).  May be state_in itself.
+ *   flags        TTT_FLAG_SILU (act = silu) or 0 (identity).
+ *   out          as x, dtype.
+ */
+int ttt_causal_conv_forward(const void* x, const float* weight, const float* bias, const long long* strides,
+                            const int* cu_seqlens, const void* state_in, void* state_out, const int* pages,
+                            int n_pages, int n_seq, long long L, int dim, int width, int dtype, unsigned int flags,
+                            void* out, void* stream);
+
+/*
+ * ttt_causal_conv_step -- one token of each sequence: x, out [n_seq, dim]; state (the pool above) is
+ * read and moved on by one row in place.  strides: NULL or the batch strides of x, out.
+ */
+int ttt_causal_conv_step(const void* x, const float* weight, const float* bias, const long long* strides, void* state,
+                         const int* pages, int n_pages, int n_seq, int dim, int width, int dtype, unsigned int flags,
+                         void* out, void* stream);
+
+/* Bytes of device workspace of ttt_causal_conv_backward (packed: 1 with cu_seqlens).  Host-only. */
+long long ttt_causal_conv_backward_workspace_bytes(int n_seq, long long L, int dim, int width, int packed, int dtype);
+
+/*
+ * ttt_causal_conv_backward -- gradients of ttt_causal_conv_forward (x, weight, bias, cu_seqlens, flags
+ * as there) for the gradient d_out of out and d_state_out of state_out.
+ *   strides      x, d_out.
+ *   state_in, d_state_out, d_state_in   [n_seq, width-1, dim] dtype (sequence b at b) or NULL; a NULL
+ *                state_in or d_state_out is zero, a NULL d_state_in is not wanted.
+ *   dx           contiguous rows like x, dtype.  d_weight [dim, width], d_bias [dim] (or NULL) float32,
+ *                summed over all rows in a fixed order.
+ *   workspace    256-byte aligned, of at least ttt_causal_conv_backward_workspace_bytes.
+ */
+int ttt_causal_conv_backward(const void* x, const float* weight, const float* bias, const long long* strides,
+                             const int* cu_seqlens, const void* state_in, int n_seq, long long L, int dim, int width,
+                             int dtype, unsigned int flags, const void* d_out, const void* d_state_out, void* dx,
+                             float* d_weight, float* d_bias, void* d_state_in, void* workspace,
+                             long long workspace_bytes, void* stream);
+
+/* Bytes of the checkpoint buffer that ttt_selective_scan_forward writes for its gradient: the state
+ * before every 8th token of each sequence, float32.  Host-only. */
+long long ttt_selective_scan_ckpt_bytes(int n_seq, long long L, int dim, int d_state, int packed);
+
+/* Bytes of device workspace of ttt_selective_scan_forward (0: none).  max_seqlen: the longest packed
+ * sequence, or 0 if it is not known (dense batches: not used).  Host-only. */
+long long ttt_selective_scan_workspace_bytes(int n_seq, long long L, long long max_seqlen, int packed, int dim,
+                                             int groups, int d_state);
+
+/*
+ * ttt_selective_scan_forward -- the selective state space scan.  Per channel d of group g, with
+ * dt = softplus(delta + delta_bias) (TTT_FLAG_SOFTPLUS) or delta + delta_bias, and n < d_state:
+ *   h[d][n] = exp(dt A[d][n]) h[d][n] + dt u[d] B[g][n]
+ *   y[d]    = sum_n C[g][n] h[d][n] + D[d] u[d],      out[d] = y[d] silu(z[d])  (y[d] without z).
+ *   u, delta, z  [n_seq, L, dim] dtype (or packed); z may be NULL.
+ *   A            [dim, d_state] float32, 16-byte aligned, d_state <= 64.
+ *   B, C         [n_seq, L, groups, d_state] dtype (or packed); channels d of group d / (dim/groups).
+ *   D, delta_bias  [dim] float32 or NULL (zero).
+ *   strides      u, delta, B, C, z, out.
+ *   max_seqlen   as in ttt_selective_scan_workspace_bytes: it chooses how the work is cut up, and a
+ *                wrong value costs time, not correctness.
+ *   state_in, state_out  pools [n_pages, dim, d_state] float32, 16-byte aligned, or NULL (zeros; not
+ *                wanted).  state_out may be state_in itself.
+ *   out          as u, dtype.
+ *   ckpt         NULL, or the buffer of ttt_selective_scan_ckpt_bytes, 16-byte aligned: written for
+ *                ttt_selective_scan_backward.
+ *   workspace    256-byte aligned, of at least ttt_selective_scan_workspace_bytes (NULL if that is 0).
+ * Few long sequences are cut into spans of tokens that run side by side (two launches); results then
+ * differ from those of whole sequences in rounding only.
+ */
+int ttt_selective_scan_forward(const void* u, const void* delta, const float* A, const void* B, const void* C,
+                               const float* D, const void* z, const float* delta_bias, const long long* strides,
+                               const int* cu_seqlens, long long max_seqlen, const float* state_in, float* state_out,
+                               const int* pages, int n_pages, int n_seq, long long L, int dim, int groups, int d_state,
+                               int dtype, unsigned int flags, void* out, float* ckpt, void* workspace,
+                               long long workspace_bytes, void* stream);
+
+/*
+ * ttt_selective_scan_step -- one token of each sequence: u, delta, z, out [n_seq, dim], B, C [n_seq,
+ * groups, d_state]; state (the pool above) is read and written in place.  strides: NULL or the batch
+ * strides of u, delta, B, C, z, out.
+ */
+int ttt_selective_scan_step(const void* u, const void* delta, const float* A, const void* B, const void* C,
+                            const float* D, const void* z, const float* delta_bias, const long long* strides,
+                            float* state, const int* pages, int n_pages, int n_seq, int dim, int groups, int d_state,
+                            int dtype, unsigned int flags, void* out, void* stream);
+
+/* Bytes of device workspace of ttt_selective_scan_backward.  Host-only. */
+long long ttt_selective_scan_backward_workspace_bytes(int n_seq, long long L, int packed, int dim, int groups,
+                                                      int d_state);
+
+/*
+ * ttt_selective_scan_backward -- gradients of ttt_selective_scan_forward (the inputs as there) for the
+ * gradient d_out of out and d_state_out of the states after each sequence.
+ *   strides      u, delta, B, C, z, d_out.
+ *   ckpt         as written by ttt_selective_scan_forward for these inputs.
+ *   d_state_out, d_state_in  [n_seq, dim, d_state] float32, 16-byte aligned (sequence b at b), or NULL
+ *                (zero; not wanted).
+ *   du, d_delta, dz  contiguous rows like u, dtype (dz with z only).  dB, dC contiguous like B, C, dtype,
+ *                summed over the channels of a group.
+ *   dA [dim, d_state], dD, d_delta_bias [dim] float32 (the last two may be NULL), summed over all rows.
+ *   workspace    256-byte aligned, of at least ttt_selective_scan_backward_workspace_bytes.
+ * All sums run in a fixed order: the same call gives the same bits.
+ */
+int ttt_selective_scan_backward(const void* u, const void* delta, const float* A, const void* B, const void* C,
+                                const float* D, const void* z, const float* delta_bias, const long long* strides,
+                                const int* cu_seqlens, const float* ckpt, int n_seq, long long L, int dim, int groups,
+                                int d_state, int dtype, unsigned int flags, const void* d_out,
+                                const float* d_state_out, void* du, void* d_delta, float* dA, void* dB, void* dC,
+                                float* dD, void* dz, float* d_delta_bias, float* d_state_in, void* workspace,
+                                long long workspace_bytes, void* stream);
+
+/* ---- pages of a cache of recurrent states ------------------------------------------------------
+ * A cache is up to 64 tensors (HOST arrays of device pointers and of bytes per page), each [n_pages,
+ * ...] contiguous with one page a sequence: the decode caches of ttt_linear_decode_step and
+ * ttt_linear_decode_step_hist (W, b, W_grad or hist, b_grad), the states of ttt_causal_conv_step and
+ * ttt_selective_scan_step, of one layer or of several.  Two int32 arrays on the device keep the books:
+ *   table [n_rows]   the page of each sequence row, or negative;
+ *   owner [n_pages]  the sequence row of each page, or negative (free).
+ * They start out as -1 throughout and are changed by these calls only.  Everything is decided on the
+ * device (no call waits for it, all may be captured), in the order of the requests: the outcome does
+ * not depend on timing.  Indexes outside the arrays are refused on the device, request by request.
+ * Pages may be of any size; pages and tensors aligned to 16 bytes copy fastest.
+ * (No counterpart on the pages under study beyond TTTCache itself.) */
+
+/*
+ * ttt_cache_copy -- page dst[i] = page src[i], i < n <= n_pages.  A pair is made (copied[i] = 1) if both
+ * indexes are pages, they differ, dst[i] is not an earlier pair's destination and not any pair's
+ * source; otherwise copied[i] = 0.  src, dst, copied: int32 [n].  workspace: int32 [1 + 2 n].
+ */
+int ttt_cache_copy(void* const* tensors, const long long* page_bytes, int n_tensors, int n_pages, const int* src,
+                   const int* dst, int n, int* copied, int* workspace, void* stream);
+
+/*
+ * ttt_cache_fork -- request i gives sequence row children[i] the lowest free page and a copy of the
+ * state of row parents[i], or zeros if parents[i] is -1 (a new sequence).  A request counts if
+ * children[i] is a row without a page, no earlier request that counts names it, and parents[i] is -1 or a row that has
+ * a page before the call.  pages[i] receives the page, or -1 (the request does not count, or no page is
+ * left: pages go to the requests in their order).  parents, children, pages: int32 [n].
+ * workspace: int32 [1 + 2 n].
+ */
+int ttt_cache_fork(void* const* tensors, const long long* page_bytes, int n_tensors, int n_pages, int* table,
+                   int n_rows, int* owner, const int* parents, const int* children, int n, int* pages, int* workspace,
+                   void* stream);
+
+/*
+ * ttt_cache_free -- the rows' pages become free; rows without one are passed over.  freed: int32 [1],
+ * receives the number of pages freed.  rows: int32 [n].
+ */
+int ttt_cache_free(int* table, int n_rows, int* owner, int n_pages, const int* rows, int n, int* freed, void* stream);
+
+/*
+ * ttt_cache_compact -- move the live pages to the front: with live[0] of them, those at or past live[0]
+ * move into the free pages below it, both lowest first.  Then the first live[0] pages are a dense
+ * batch for the decode steps, page p holding sequence row owner[p].  new_page: int32 [n_pages], the
+ * new page of each old one (-1: it was free).  workspace: int32 [2 + n_pages].
+ */
+int ttt_cache_compact(void* const* tensors, const long long* page_bytes, int n_tensors, int n_pages, int* table,
+                      int n_rows, int* owner, int* live, int* new_page, int* workspace, void* stream);
 
 #ifdef __cplusplus
 }

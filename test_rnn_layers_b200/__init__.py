@@ -29,6 +29,8 @@ TTT_BF16 = 1
 TTT_FLAG_FP32_COMPUTE = 1
 TTT_FLAG_TOKEN_MAJOR = 2
 TTT_FLAG_ROPE_HALF_SPLIT = 4
+TTT_FLAG_SOFTPLUS = 8
+TTT_FLAG_SILU = 16
 TTT_STATUS_TIMEOUT = 1
 TTT_STATIC_SCRATCH_BYTES = 33554432
 
@@ -37,7 +39,11 @@ EXPORTS = ("ttt_partition", "ttt_error_string", "ttt_last_error_message", "ttt_d
            "ttt_linear_forward_host", "ttt_linear_forward_host_static", "ttt_mlp_forward",
            "ttt_linear_decode_step", "ttt_linear_decode_step_hist", "ttt_o_proj_prepare", "ttt_post_norm_o_proj",
            "ttt_linear_backward_workspace_bytes", "ttt_linear_backward", "ttt_linear_ckpt_bytes",
-           "ttt_linear_forward_ckpt", "ttt_linear_backward_ckpt")
+           "ttt_linear_forward_ckpt", "ttt_linear_backward_ckpt",
+           "ttt_causal_conv_forward", "ttt_causal_conv_step", "ttt_causal_conv_backward_workspace_bytes",
+           "ttt_causal_conv_backward", "ttt_selective_scan_ckpt_bytes", "ttt_selective_scan_workspace_bytes",
+           "ttt_selective_scan_forward", "ttt_selective_scan_step", "ttt_selective_scan_backward_workspace_bytes",
+           "ttt_selective_scan_backward", "ttt_cache_copy", "ttt_cache_fork", "ttt_cache_free", "ttt_cache_compact")
 
 
 class TTTError(RuntimeError):
@@ -94,6 +100,31 @@ def lib():
                                               vp, fp, fp, fp, fp, i, fp, vp]
         L.ttt_linear_backward_ckpt.argtypes = [vp, vp, vp, fp, fp, fp, fp, ll, fp, fp, i, i, ll, i, i, f, i, u, i, fp,
                                                vp, fp, fp, vp, vp, vp, fp, fp, fp, fp, fp, vp, ll, vp]
+        pp, pl = ctypes.POINTER(vp), ctypes.POINTER(ll)
+        L.ttt_causal_conv_forward.argtypes = [vp, fp, fp, pl, vp, vp, vp, vp, i, i, ll, i, i, i, u, vp, vp]
+        L.ttt_causal_conv_step.argtypes = [vp, fp, fp, pl, vp, vp, i, i, i, i, i, u, vp, vp]
+        L.ttt_causal_conv_backward_workspace_bytes.argtypes = [i, ll, i, i, i, i]
+        L.ttt_causal_conv_backward.argtypes = [vp, fp, fp, pl, vp, vp, i, ll, i, i, i, u, vp, vp, vp, fp, fp, vp, vp, ll,
+                                               vp]
+        L.ttt_selective_scan_ckpt_bytes.argtypes = [i, ll, i, i, i]
+        L.ttt_selective_scan_workspace_bytes.argtypes = [i, ll, ll, i, i, i, i]
+        L.ttt_selective_scan_forward.argtypes = [vp, vp, fp, vp, vp, fp, vp, fp, pl, vp, ll, fp, fp, vp, i, i, ll, i, i,
+                                                 i, i, u, vp, fp, vp, ll, vp]
+        L.ttt_selective_scan_step.argtypes = [vp, vp, fp, vp, vp, fp, vp, fp, pl, fp, vp, i, i, i, i, i, i, u, vp, vp]
+        L.ttt_selective_scan_backward_workspace_bytes.argtypes = [i, ll, i, i, i, i]
+        L.ttt_selective_scan_backward.argtypes = [vp, vp, fp, vp, vp, fp, vp, fp, pl, vp, fp, i, ll, i, i, i, i, u, vp,
+                                                  fp, vp, vp, fp, vp, vp, fp, vp, fp, fp, vp, ll, vp]
+        L.ttt_cache_copy.argtypes = [pp, pl, i, i, vp, vp, i, vp, vp, vp]
+        L.ttt_cache_fork.argtypes = [pp, pl, i, i, vp, i, vp, vp, vp, i, vp, vp, vp]
+        L.ttt_cache_free.argtypes = [vp, i, vp, i, vp, i, vp, vp]
+        L.ttt_cache_compact.argtypes = [pp, pl, i, i, vp, i, vp, vp, vp, vp, vp]
+        for name in ("ttt_causal_conv_backward_workspace_bytes", "ttt_selective_scan_ckpt_bytes",
+                     "ttt_selective_scan_workspace_bytes", "ttt_selective_scan_backward_workspace_bytes"):
+            getattr(L, name).restype = ll
+        for name in ("ttt_causal_conv_forward", "ttt_causal_conv_step", "ttt_causal_conv_backward",
+                     "ttt_selective_scan_forward", "ttt_selective_scan_step", "ttt_selective_scan_backward",
+                     "ttt_cache_copy", "ttt_cache_fork", "ttt_cache_free", "ttt_cache_compact"):
+            getattr(L, name).restype = ctypes.c_int
         for name in ("ttt_partition", "ttt_device_status", "ttt_set_wait_limit", "ttt_linear_forward",
                      "ttt_o_proj_prepare", "ttt_post_norm_o_proj",
                      "ttt_linear_forward_rope",
@@ -563,3 +594,403 @@ def ttt_linear_backward(XQ, XK, XV, lr, W0, b0, ln_w, ln_b, d_out, dW_last=None,
             raise ValueError("ckpt is smaller than ttt_linear_ckpt_bytes(...)")
         _check(lib().ttt_linear_backward_ckpt(*head, _ptr(ckpt), *tail))
     return g
+
+
+# ---- causal convolution, selective scan, cache pages -------------------------------------------------
+
+class _On:
+    """The device and stream of a call: its tensors' device is made current, and what the call
+    allocates belongs to the stream it runs on."""
+
+    def __init__(self, t, stream):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("the first argument must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError("the tensors must be CUDA tensors (there is no CPU path)")
+        self.device = t.device
+        self.stream = torch.cuda.current_stream(t.device) if stream is None else stream
+        if self.stream.device != t.device:
+            raise ValueError(f"the stream is on {self.stream.device}, the tensors on {t.device}")
+        self._ctx = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        self._ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        return self._ctx.__exit__(*exc)
+
+    def need(self, t, name, dtype=None, shape=None):
+        _need(t, name, dtype, shape)
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the first argument on {self.device}")
+        return t
+
+    def maybe(self, t, name, dtype=None, shape=None):
+        return None if t is None else self.need(t, name, dtype, shape)
+
+    def rows(self, t, name, dtype, shape, inner: int = 1):
+        """t's (batch, token) element strides; its last `inner` dimensions must be contiguous."""
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the first argument on {self.device}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        want = 1
+        for k in range(1, inner + 1):
+            if t.shape[-k] > 1 and t.stride(-k) != want:
+                raise ValueError(f"{name}: its channels must be contiguous, got strides {tuple(t.stride())}")
+            want *= t.shape[-k]
+        lead = t.stride()[:-inner]
+        return (0, *lead) if len(lead) == 1 else lead
+
+    def workspace(self, nbytes: int, given=None):
+        if given is not None:
+            return self.need(given, "workspace", torch.uint8)
+        return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+
+    @property
+    def handle(self):
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+
+def _strides(*pairs):
+    flat = [int(s) for p in pairs for s in p]
+    return (ctypes.c_longlong * len(flat))(*flat)
+
+
+def _bytes(n) -> int:
+    if n < 0:
+        _check(int(n))
+    return int(n)
+
+
+def _seq_sizes(x, name, cu_seqlens):
+    """(n_seq, L, leading shape) of rows [n_seq, L, dim], or packed rows [L, dim] with cu_seqlens."""
+    if cu_seqlens is None:
+        if x.dim() != 3:
+            raise ValueError(f"{name} must be [n_seq, L, dim] (packed rows [L, dim] need cu_seqlens), got {tuple(x.shape)}")
+        return x.shape[0], x.shape[1], tuple(x.shape[:2])
+    if x.dim() != 2:
+        raise ValueError(f"with cu_seqlens {name} must be packed rows [L, dim], got {tuple(x.shape)}")
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be an int32 tensor [n_seq + 1]")
+    return cu_seqlens.numel() - 1, x.shape[0], (x.shape[0],)
+
+
+def _new_rows(shape, dtype, device, cu_seqlens):
+    """An output: rows past the last packed sequence are not written, so they start as zeros."""
+    return torch.empty(shape, dtype=dtype, device=device) if cu_seqlens is None else torch.zeros(shape, dtype=dtype, device=device)
+
+
+def _pool(on, pages, n_seq, *pools):
+    """Pages of the state pools given (each None or [n_pages, ...])."""
+    on.maybe(pages, "pages", torch.int32, (n_seq,))
+    sizes = {p.shape[0] for p in pools if p is not None}
+    if len(sizes) > 1:
+        raise ValueError("state_in and state_out must have the same number of pages")
+    return sizes.pop() if sizes else 0
+
+
+def ttt_causal_conv_forward(x, weight, bias=None, silu: bool = True, state_in=None, state_out=None, pages=None,
+                            cu_seqlens=None, out=None, stream=None):
+    """Short causal convolution over tokens (one filter of 2 to 4 taps a channel, then silu): x [n_seq, L,
+    dim], or packed rows [L, dim] with cu_seqlens (int32 [n_seq + 1]); weight [dim, width], bias [dim]
+    float32.  state_in / state_out: pools [n_pages, width - 1, dim] in x's dtype holding the inputs
+    before / after each sequence, in the pages named by `pages` (int32 [n_seq], default page b).
+    x may be a strided view with contiguous channels.  Returns out (see include/ttt.h)."""
+    with _On(x, stream) as on:
+        n_seq, L, lead = _seq_sizes(x, "x", cu_seqlens)
+        dim = x.shape[-1]
+        sx = on.rows(x, "x", x.dtype, (*lead, dim))
+        if weight.dim() != 2:
+            raise ValueError("weight must be [dim, width]")
+        width = weight.shape[1]
+        on.need(weight, "weight", torch.float32, (dim, width))
+        on.maybe(bias, "bias", torch.float32, (dim,))
+        on.maybe(cu_seqlens, "cu_seqlens", torch.int32)
+        n_pages = _pool(on, pages, n_seq, state_in, state_out)
+        for n, t in (("state_in", state_in), ("state_out", state_out)):
+            on.maybe(t, n, x.dtype, (n_pages, width - 1, dim))
+        if out is None:
+            out = _new_rows(x.shape, x.dtype, on.device, cu_seqlens)
+        so = on.rows(out, "out", x.dtype, x.shape)
+        _check(lib().ttt_causal_conv_forward(_ptr(x), _ptr(weight), _ptr(bias), _strides(sx, so), _ptr(cu_seqlens),
+                                             _ptr(state_in), _ptr(state_out), _ptr(pages), n_pages, n_seq, L, dim,
+                                             width, _dtype_code(x), TTT_FLAG_SILU if silu else 0, _ptr(out), on.handle))
+        return out
+
+
+def ttt_causal_conv_step(x, state, weight, bias=None, silu: bool = True, pages=None, out=None, stream=None):
+    """One token of each sequence through the convolution: x [n_seq, dim]; `state` (a pool [n_pages, width
+    - 1, dim]) moves on by one row in place.  Rows whose page is negative are left out.  Returns out."""
+    with _On(x, stream) as on:
+        if x.dim() != 2:
+            raise ValueError(f"x must be [n_seq, dim], got {tuple(x.shape)}")
+        n_seq, dim = x.shape
+        sx = on.rows(x, "x", x.dtype, (n_seq, dim))
+        if weight.dim() != 2:
+            raise ValueError("weight must be [dim, width]")
+        width = weight.shape[1]
+        on.need(weight, "weight", torch.float32, (dim, width))
+        on.maybe(bias, "bias", torch.float32, (dim,))
+        n_pages = _pool(on, pages, n_seq, state)
+        on.need(state, "state", x.dtype, (n_pages, width - 1, dim))
+        if out is None:
+            out = torch.empty((n_seq, dim), dtype=x.dtype, device=on.device) if pages is None else \
+                torch.zeros((n_seq, dim), dtype=x.dtype, device=on.device)
+        so = on.rows(out, "out", x.dtype, (n_seq, dim))
+        _check(lib().ttt_causal_conv_step(_ptr(x), _ptr(weight), _ptr(bias), _strides(sx[1:], so[1:]), _ptr(state),
+                                          _ptr(pages), n_pages, n_seq, dim, width, _dtype_code(x),
+                                          TTT_FLAG_SILU if silu else 0, _ptr(out), on.handle))
+        return out
+
+
+def ttt_causal_conv_backward_workspace_bytes(n_seq: int, L: int, dim: int, width: int, packed: bool = False,
+                                             dtype=torch.bfloat16) -> int:
+    """Bytes of device workspace that ttt_causal_conv_backward needs (host-only)."""
+    return _bytes(lib().ttt_causal_conv_backward_workspace_bytes(n_seq, L, dim, width, int(packed),
+                                                                 TTT_F32 if dtype == torch.float32 else TTT_BF16))
+
+
+def ttt_causal_conv_backward(x, weight, d_out, bias=None, silu: bool = True, state_in=None, d_state_out=None,
+                             cu_seqlens=None, workspace=None, stream=None):
+    """Gradients of ttt_causal_conv_forward for d_out (and d_state_out, the gradient of the states after
+    each sequence; state_in and d_state_out are [n_seq, width - 1, dim] here, sequence b at b).  Returns a
+    dict: dx (x's dtype), dweight [dim, width], dbias [dim] float32 (None without bias), dstate_in (None
+    without state_in)."""
+    with _On(x, stream) as on:
+        n_seq, L, lead = _seq_sizes(x, "x", cu_seqlens)
+        dim = x.shape[-1]
+        sx = on.rows(x, "x", x.dtype, (*lead, dim))
+        sd = on.rows(d_out, "d_out", x.dtype, x.shape)
+        if weight.dim() != 2:
+            raise ValueError("weight must be [dim, width]")
+        width = weight.shape[1]
+        on.need(weight, "weight", torch.float32, (dim, width))
+        on.maybe(bias, "bias", torch.float32, (dim,))
+        on.maybe(cu_seqlens, "cu_seqlens", torch.int32)
+        for n, t in (("state_in", state_in), ("d_state_out", d_state_out)):
+            on.maybe(t, n, x.dtype, (n_seq, width - 1, dim))
+        ws = on.workspace(ttt_causal_conv_backward_workspace_bytes(n_seq, L, dim, width, cu_seqlens is not None, x.dtype),
+                          workspace)
+        g = {"dx": _new_rows(x.shape, x.dtype, on.device, cu_seqlens),
+             "dweight": torch.empty((dim, width), device=on.device),
+             "dbias": None if bias is None else torch.empty(dim, device=on.device),
+             "dstate_in": None if state_in is None else torch.empty_like(state_in)}
+        _check(lib().ttt_causal_conv_backward(_ptr(x), _ptr(weight), _ptr(bias), _strides(sx, sd), _ptr(cu_seqlens),
+                                              _ptr(state_in), n_seq, L, dim, width, _dtype_code(x),
+                                              TTT_FLAG_SILU if silu else 0, _ptr(d_out), _ptr(d_state_out),
+                                              _ptr(g["dx"]), _ptr(g["dweight"]), _ptr(g["dbias"]), _ptr(g["dstate_in"]),
+                                              _ptr(ws), ws.numel(), on.handle))
+        return g
+
+
+def ttt_selective_scan_ckpt_bytes(n_seq: int, L: int, dim: int, d_state: int, packed: bool = False) -> int:
+    """Bytes of the checkpoint buffer of ttt_selective_scan_forward(..., ckpt=) (host-only)."""
+    return _bytes(lib().ttt_selective_scan_ckpt_bytes(n_seq, L, dim, d_state, int(packed)))
+
+
+def ttt_selective_scan_workspace_bytes(n_seq: int, L: int, dim: int, d_state: int, groups: int = 1,
+                                       packed: bool = False, max_seqlen: int = 0) -> int:
+    """Bytes of device workspace that ttt_selective_scan_forward needs, perhaps 0 (host-only)."""
+    return _bytes(lib().ttt_selective_scan_workspace_bytes(n_seq, L, max_seqlen, int(packed), dim, groups, d_state))
+
+
+def ttt_selective_scan_backward_workspace_bytes(n_seq: int, L: int, dim: int, d_state: int, groups: int = 1,
+                                                packed: bool = False) -> int:
+    """Bytes of device workspace that ttt_selective_scan_backward needs (host-only)."""
+    return _bytes(lib().ttt_selective_scan_backward_workspace_bytes(n_seq, L, int(packed), dim, groups, d_state))
+
+
+def _scan_operands(on, u, delta, A, B, C, D, z, delta_bias, lead):
+    """Check the scan's inputs (rows of shape `lead`): (dim, groups, d_state, their row strides)."""
+    dim, dt = u.shape[-1], u.dtype
+    if A.dim() != 2:
+        raise ValueError("A must be [dim, d_state]")
+    N = A.shape[1]
+    on.need(A, "A", torch.float32, (dim, N))
+    if B.dim() != len(lead) + 2:
+        raise ValueError(f"B must be {(*lead, 'groups', 'd_state')}, got {tuple(B.shape)}")
+    G = B.shape[-2]
+    s = [on.rows(u, "u", dt, (*lead, dim)), on.rows(delta, "delta", dt, (*lead, dim)),
+         on.rows(B, "B", dt, (*lead, G, N), 2), on.rows(C, "C", dt, (*lead, G, N), 2),
+         (0, 0) if z is None else on.rows(z, "z", dt, (*lead, dim))]
+    on.maybe(D, "D", torch.float32, (dim,))
+    on.maybe(delta_bias, "delta_bias", torch.float32, (dim,))
+    return dim, G, N, s
+
+
+def _check_ckpt(on, ckpt, n_seq, L, dim, N, packed):
+    on.need(ckpt, "ckpt", torch.float32)
+    if ckpt.numel() * 4 < ttt_selective_scan_ckpt_bytes(n_seq, L, dim, N, packed):
+        raise ValueError("ckpt is smaller than ttt_selective_scan_ckpt_bytes(...)")
+
+
+def ttt_selective_scan_forward(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus: bool = True,
+                               state_in=None, state_out=None, pages=None, cu_seqlens=None, max_seqlen: int = 0,
+                               ckpt=None, out=None, workspace=None, stream=None):
+    """Selective state space scan: u, delta, z [n_seq, L, dim] and B, C [n_seq, L, groups, d_state], or packed
+    rows ([L, dim], [L, groups, d_state]) with cu_seqlens; A [dim, d_state], D, delta_bias [dim] float32.
+    state_in / state_out: float32 pools [n_pages, dim, d_state], in the pages named by `pages` (int32
+    [n_seq], default page b).  max_seqlen: the longest packed sequence, if known (it only guides how the
+    work is cut up).  ckpt: a float32 tensor of ttt_selective_scan_ckpt_bytes bytes to receive what
+    ttt_selective_scan_backward needs.  Activations may be strided views with contiguous channels.
+    Returns out (see include/ttt.h)."""
+    with _On(u, stream) as on:
+        n_seq, L, lead = _seq_sizes(u, "u", cu_seqlens)
+        dim, G, N, s = _scan_operands(on, u, delta, A, B, C, D, z, delta_bias, lead)
+        packed = cu_seqlens is not None
+        on.maybe(cu_seqlens, "cu_seqlens", torch.int32)
+        n_pages = _pool(on, pages, n_seq, state_in, state_out)
+        for n, t in (("state_in", state_in), ("state_out", state_out)):
+            on.maybe(t, n, torch.float32, (n_pages, dim, N))
+        if ckpt is not None:
+            _check_ckpt(on, ckpt, n_seq, L, dim, N, packed)
+        if out is None:
+            out = _new_rows(u.shape, u.dtype, on.device, cu_seqlens)
+        s.append(on.rows(out, "out", u.dtype, u.shape))
+        need = ttt_selective_scan_workspace_bytes(n_seq, L, dim, N, G, packed, max_seqlen)
+        ws = on.workspace(need, workspace) if need or workspace is not None else None
+        _check(lib().ttt_selective_scan_forward(_ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+                                                _ptr(delta_bias), _strides(*s), _ptr(cu_seqlens), max_seqlen,
+                                                _ptr(state_in), _ptr(state_out), _ptr(pages), n_pages, n_seq, L, dim,
+                                                G, N, _dtype_code(u), TTT_FLAG_SOFTPLUS if softplus else 0, _ptr(out),
+                                                _ptr(ckpt), _ptr(ws), 0 if ws is None else ws.numel(), on.handle))
+        return out
+
+
+def ttt_selective_scan_step(u, delta, A, B, C, state, D=None, z=None, delta_bias=None, softplus: bool = True,
+                            pages=None, out=None, stream=None):
+    """One token of each sequence through the scan: u, delta, z [n_seq, dim], B, C [n_seq, groups, d_state];
+    `state` (a float32 pool [n_pages, dim, d_state]) is updated in place.  Rows whose page is negative are
+    left out.  Returns out."""
+    with _On(u, stream) as on:
+        if u.dim() != 2:
+            raise ValueError(f"u must be [n_seq, dim], got {tuple(u.shape)}")
+        n_seq = u.shape[0]
+        dim, G, N, s = _scan_operands(on, u, delta, A, B, C, D, z, delta_bias, (n_seq,))
+        n_pages = _pool(on, pages, n_seq, state)
+        on.need(state, "state", torch.float32, (n_pages, dim, N))
+        if out is None:
+            out = torch.empty((n_seq, dim), dtype=u.dtype, device=on.device) if pages is None else \
+                torch.zeros((n_seq, dim), dtype=u.dtype, device=on.device)
+        s.append(on.rows(out, "out", u.dtype, u.shape))
+        _check(lib().ttt_selective_scan_step(_ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+                                             _ptr(delta_bias), _strides(*[p[1:] for p in s]), _ptr(state), _ptr(pages),
+                                             n_pages, n_seq, dim, G, N, _dtype_code(u),
+                                             TTT_FLAG_SOFTPLUS if softplus else 0, _ptr(out), on.handle))
+        return out
+
+
+def ttt_selective_scan_backward(u, delta, A, B, C, d_out, ckpt, D=None, z=None, delta_bias=None, softplus: bool = True,
+                                d_state_out=None, state_in_grad: bool = False, cu_seqlens=None, workspace=None,
+                                stream=None):
+    """Gradients of ttt_selective_scan_forward for d_out (and d_state_out [n_seq, dim, d_state], the gradient
+    of the states after each sequence), from the ckpt that the forward wrote.  Returns a dict: du, ddelta,
+    dB, dC, dz (the activations' dtype), dA, dD, ddelta_bias float32, and dstate_in [n_seq, dim, d_state] with
+    state_in_grad; None for inputs that are None."""
+    with _On(u, stream) as on:
+        n_seq, L, lead = _seq_sizes(u, "u", cu_seqlens)
+        dim, G, N, s = _scan_operands(on, u, delta, A, B, C, D, z, delta_bias, lead)
+        packed = cu_seqlens is not None
+        on.maybe(cu_seqlens, "cu_seqlens", torch.int32)
+        s.append(on.rows(d_out, "d_out", u.dtype, u.shape))
+        _check_ckpt(on, ckpt, n_seq, L, dim, N, packed)
+        on.maybe(d_state_out, "d_state_out", torch.float32, (n_seq, dim, N))
+        ws = on.workspace(ttt_selective_scan_backward_workspace_bytes(n_seq, L, dim, N, G, packed), workspace)
+        rows = lambda t: _new_rows(t.shape, u.dtype, on.device, cu_seqlens)
+        g = {"du": rows(u), "ddelta": rows(u), "dA": torch.empty((dim, N), device=on.device), "dB": rows(B),
+             "dC": rows(C), "dD": None if D is None else torch.empty(dim, device=on.device),
+             "dz": None if z is None else rows(u),
+             "ddelta_bias": None if delta_bias is None else torch.empty(dim, device=on.device),
+             "dstate_in": torch.empty((n_seq, dim, N), device=on.device) if state_in_grad else None}
+        _check(lib().ttt_selective_scan_backward(_ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+                                                 _ptr(delta_bias), _strides(*s), _ptr(cu_seqlens), _ptr(ckpt), n_seq, L,
+                                                 dim, G, N, _dtype_code(u), TTT_FLAG_SOFTPLUS if softplus else 0,
+                                                 _ptr(d_out), _ptr(d_state_out), _ptr(g["du"]), _ptr(g["ddelta"]),
+                                                 _ptr(g["dA"]), _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g["dD"]),
+                                                 _ptr(g["dz"]), _ptr(g["ddelta_bias"]), _ptr(g["dstate_in"]), _ptr(ws),
+                                                 ws.numel(), on.handle))
+        return g
+
+
+def _cache_tensors(on, tensors, n_pages):
+    ptrs = (ctypes.c_void_p * max(1, len(tensors)))()
+    sizes = (ctypes.c_longlong * max(1, len(tensors)))()
+    for k, t in enumerate(tensors):
+        on.need(t, f"tensors[{k}]")
+        if t.dim() < 1 or t.shape[0] != n_pages:
+            raise ValueError(f"tensors[{k}] must have {n_pages} pages (its first dimension), got {tuple(t.shape)}")
+        ptrs[k] = t.data_ptr()
+        sizes[k] = t.numel() // n_pages * t.element_size()
+    return ptrs, sizes, len(tensors)
+
+
+def ttt_cache_copy(tensors, src, dst, stream=None):
+    """Copy pages: page dst[i] of every tensor (each [n_pages, ...]) becomes page src[i].  Returns copied
+    (int32 [n]): 0 where a pair was refused (an index outside the cache, a destination named before or
+    also named as a source)."""
+    with _On(src, stream) as on:
+        if not tensors:
+            raise ValueError("tensors must name at least one tensor")
+        n, n_pages = src.numel(), tensors[0].shape[0]
+        on.need(src, "src", torch.int32, (n,))
+        on.need(dst, "dst", torch.int32, (n,))
+        t = _cache_tensors(on, tensors, n_pages)
+        copied = torch.empty(n, dtype=torch.int32, device=on.device)
+        ws = torch.empty(1 + 2 * n, dtype=torch.int32, device=on.device)
+        _check(lib().ttt_cache_copy(*t, n_pages, _ptr(src), _ptr(dst), n, _ptr(copied), _ptr(ws), on.handle))
+        return copied
+
+
+def ttt_cache_fork(tensors, table, owner, parents, children, stream=None):
+    """Give each row children[i] the lowest free page and a copy of the state of row parents[i] (zeros for
+    a parent of -1: a new sequence).  table: int32 [n_rows], the page of each sequence row; owner: int32
+    [n_pages], the row of each page; both -1 where there is none, and updated in place.  Returns pages
+    (int32 [n]): the page given to each request, or -1."""
+    with _On(table, stream) as on:
+        n = children.numel()
+        n_rows, n_pages = table.numel(), owner.numel()
+        on.need(table, "table", torch.int32, (n_rows,))
+        on.need(owner, "owner", torch.int32, (n_pages,))
+        on.need(parents, "parents", torch.int32, (n,))
+        on.need(children, "children", torch.int32, (n,))
+        t = _cache_tensors(on, tensors, n_pages)
+        pages = torch.empty(n, dtype=torch.int32, device=on.device)
+        ws = torch.empty(1 + 2 * n, dtype=torch.int32, device=on.device)
+        _check(lib().ttt_cache_fork(*t, n_pages, _ptr(table), n_rows, _ptr(owner), _ptr(parents), _ptr(children), n,
+                                    _ptr(pages), _ptr(ws), on.handle))
+        return pages
+
+
+def ttt_cache_free(table, owner, rows, stream=None):
+    """Free the pages of the sequence rows (int32 [n]).  Returns the number freed (an int32 tensor)."""
+    with _On(table, stream) as on:
+        n, n_rows, n_pages = rows.numel(), table.numel(), owner.numel()
+        on.need(table, "table", torch.int32, (n_rows,))
+        on.need(owner, "owner", torch.int32, (n_pages,))
+        on.need(rows, "rows", torch.int32, (n,))
+        freed = torch.empty((), dtype=torch.int32, device=on.device)
+        _check(lib().ttt_cache_free(_ptr(table), n_rows, _ptr(owner), n_pages, _ptr(rows), n, _ptr(freed), on.handle))
+        return freed
+
+
+def ttt_cache_compact(tensors, table, owner, stream=None):
+    """Move the live pages to the front, so that the first `live` pages are a dense batch for the decode
+    steps.  Returns (live, new_page): the number of live pages (an int32 tensor) and the new page of each
+    old one (int32 [n_pages], -1 where it was free)."""
+    with _On(table, stream) as on:
+        n_rows, n_pages = table.numel(), owner.numel()
+        on.need(table, "table", torch.int32, (n_rows,))
+        on.need(owner, "owner", torch.int32, (n_pages,))
+        t = _cache_tensors(on, tensors, n_pages)
+        live = torch.empty((), dtype=torch.int32, device=on.device)
+        new_page = torch.empty(n_pages, dtype=torch.int32, device=on.device)
+        ws = torch.empty(2 + n_pages, dtype=torch.int32, device=on.device)
+        _check(lib().ttt_cache_compact(*t, n_pages, _ptr(table), n_rows, _ptr(owner), _ptr(live), _ptr(new_page),
+                                       _ptr(ws), on.handle))
+        return live, new_page

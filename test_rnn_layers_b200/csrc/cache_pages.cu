@@ -1,0 +1,286 @@
+// cache_pages.cu -- the pages of a cache of recurrent states: copying, forking, freeing, compacting.
+//
+// A cache is a set of tensors with one page (row) a sequence; `table` gives each sequence row its page
+// (-1: none) and `owner` each page its sequence row (-1: free).  Everything is decided on the device,
+// so nothing waits for the host and the calls can be captured into a graph: one block of 1024 threads
+// keeps the books (prefix sums over the requests and over the pages, in their order, so that the
+// outcome does not depend on timing) and writes the pairs (source, destination) to copy; a second
+// launch copies them.
+//
+// The copies are bound by HBM: 2 * page bytes a pair.  One CTA takes a piece of one tensor's page at
+// a time; the pieces of all pairs and tensors are dealt out over a grid that fills the GPU, with
+// kUnroll 16-byte loads in flight a thread.
+#include <limits.h>
+
+#include "seq_common.cuh"
+
+namespace ttt {
+namespace {
+
+constexpr int kBook = 1024;
+constexpr int kCopy = 256, kUnroll = 4;
+constexpr long long kPiece = 16ll * kCopy * kUnroll;   // bytes a CTA copies at a time
+
+// Sum of `v` over the threads before this one; `total` over all of them.
+__device__ __forceinline__ int block_scan(int v, int& total) {
+    __shared__ int warp_sums[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int s = lane < kBook / 32 ? warp_sums[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        warp_sums[lane] = s;
+    }
+    __syncthreads();
+    const int before = (warp ? warp_sums[warp - 1] : 0) + x - v;
+    total = warp_sums[31];
+    __syncthreads();
+    return before;
+}
+
+// ---- copying -----------------------------------------------------------------------------------
+template <typename V>
+__device__ __forceinline__ void copy_piece(const char* src, char* dst, long long bytes) {
+    const long long n = bytes / static_cast<long long>(sizeof(V));
+    const V* s = reinterpret_cast<const V*>(src);
+    V* d = reinterpret_cast<V*>(dst);
+    for (long long i = threadIdx.x; i < n; i += static_cast<long long>(kCopy) * kUnroll) {
+        V v[kUnroll];
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k)
+            if (i + k * kCopy < n) v[k] = s[i + k * kCopy];
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k)
+            if (i + k * kCopy < n) d[i + k * kCopy] = v[k];
+    }
+}
+template <typename V>
+__device__ __forceinline__ void zero_piece(char* dst, long long bytes) {
+    const long long n = bytes / static_cast<long long>(sizeof(V));
+    V* d = reinterpret_cast<V*>(dst);
+    for (long long i = threadIdx.x; i < n; i += kCopy) d[i] = V{};
+}
+
+// moves[0] pairs (source, destination) from moves[1] on; a source of -1 zeroes the destination.
+__global__ void __launch_bounds__(kCopy) cache_copy_kernel(const CacheTensors t, const int* moves, int pieces) {
+    const int n = moves[0];
+    const long long total = static_cast<long long>(n) * pieces;
+    for (long long w = blockIdx.x; w < total; w += gridDim.x) {
+        const int pair = static_cast<int>(w / pieces);
+        int piece = static_cast<int>(w % pieces);
+        int k = 0;
+        for (; k < t.n; ++k) {  // the tensor this piece belongs to
+            const int m = static_cast<int>((t.bytes[k] + kPiece - 1) / kPiece);
+            if (piece < m) break;
+            piece -= m;
+        }
+        const long long off = piece * kPiece, bytes = min(kPiece, t.bytes[k] - off);
+        const int from = moves[1 + 2 * pair], to = moves[2 + 2 * pair];
+        char* dst = t.base[k] + to * t.bytes[k] + off;
+        const char* src = t.base[k] + from * t.bytes[k] + off;
+        const unsigned long long align = reinterpret_cast<uintptr_t>(t.base[k]) | static_cast<unsigned long long>(t.bytes[k]);
+        if (from < 0) {
+            if (align % 16 == 0) zero_piece<uint4>(dst, bytes);
+            else if (align % 4 == 0) zero_piece<uint32_t>(dst, bytes);
+            else zero_piece<char>(dst, bytes);
+        } else {
+            if (align % 16 == 0) copy_piece<uint4>(src, dst, bytes);
+            else if (align % 4 == 0) copy_piece<uint32_t>(src, dst, bytes);
+            else copy_piece<char>(src, dst, bytes);
+        }
+    }
+}
+
+// Copies by index.  A pair is made if both indexes are pages, its destination is no other pair's
+// destination before it and no pair's source (so that the order of the copies does not matter).
+__global__ void __launch_bounds__(kBook) cache_pairs_kernel(const CacheArgs a) {
+    int made = 0;
+    for (int i0 = 0; i0 < a.n; i0 += kBook) {
+        const int i = i0 + threadIdx.x;
+        bool ok = false;
+        int from = -1, to = -1;
+        if (i < a.n) {
+            from = a.a[i];
+            to = a.b[i];
+            ok = from >= 0 && from < a.n_pages && to >= 0 && to < a.n_pages && from != to;
+            for (int j = 0; ok && j < a.n; ++j) {
+                if (a.a[j] == to) ok = false;
+                if (j < i && a.b[j] == to) ok = false;
+            }
+            a.result[i] = ok ? 1 : 0;
+        }
+        int total;
+        const int at = made + block_scan(ok ? 1 : 0, total);
+        if (ok) {
+            a.moves[1 + 2 * at] = from;
+            a.moves[2 + 2 * at] = to;
+        }
+        made += total;
+    }
+    if (threadIdx.x == 0) a.moves[0] = made;
+}
+
+// ---- forking -----------------------------------------------------------------------------------
+// Request i gives row children[i], which has no page, the lowest free page, and row parents[i]'s state
+// (zeros for a parent of -1).  Of two requests for one child the first counts.
+__global__ void __launch_bounds__(kBook) cache_fork_kernel(const CacheArgs a) {
+    // A child's entry holds -1; the requests claim it with INT_MIN + i, the lowest of which stays.
+    // (Read past L1: the claims are atomics.)
+    constexpr int kClaim = INT_MIN;
+    auto valid = [&](int i, int& child, int& from) {
+        child = a.b[i];
+        const int parent = a.a[i];
+        if (child < 0 || child >= a.n_rows || parent < -1 || parent >= a.n_rows) return false;
+        from = -1;
+        if (parent >= 0) {
+            from = __ldcg(&a.table[parent]);  // a row without a page holds something negative, claimed or not
+            if (from < 0 || from >= a.n_pages) return false;
+        }
+        return true;
+    };
+    for (int i = threadIdx.x; i < a.n; i += kBook) {
+        int child, from;
+        if (valid(i, child, from) && __ldcg(&a.table[child]) < 0) atomicMin(&a.table[child], kClaim + i);
+    }
+    __syncthreads();
+    // the winning requests, in their order, packed into moves[] as (request, source)
+    int wins = 0;
+    for (int i0 = 0; i0 < a.n; i0 += kBook) {
+        const int i = i0 + threadIdx.x;
+        int child = 0, from = -1, total;
+        const bool win = i < a.n && valid(i, child, from) && __ldcg(&a.table[child]) == kClaim + i;
+        const int at = wins + block_scan(win ? 1 : 0, total);
+        if (i < a.n) a.result[i] = -1;
+        if (win) {
+            a.moves[1 + 2 * at] = from;
+            a.moves[2 + 2 * at] = i;
+        }
+        wins += total;
+    }
+    __syncthreads();
+    // the free pages, lowest first, to the requests in their order
+    int given = 0;
+    for (int p0 = 0; p0 < a.n_pages && given < wins; p0 += kBook) {
+        const int p = p0 + threadIdx.x;
+        int total;
+        const bool free = p < a.n_pages && a.owner[p] < 0;
+        const int at = given + block_scan(free ? 1 : 0, total);
+        if (free && at < wins) {
+            const int i = a.moves[2 + 2 * at], child = a.b[i];
+            a.moves[2 + 2 * at] = p;
+            a.result[i] = p;
+            a.owner[p] = child;
+            a.table[child] = p;
+        }
+        given += total;
+    }
+    __syncthreads();
+    const int made = min(given, wins);
+    for (int at = made + threadIdx.x; at < wins; at += kBook) a.table[a.b[a.moves[2 + 2 * at]]] = -1;  // no page left
+    if (threadIdx.x == 0) a.moves[0] = made;
+}
+
+// ---- freeing -----------------------------------------------------------------------------------
+__global__ void __launch_bounds__(kBook) cache_free_kernel(const CacheArgs a) {
+    int freed = 0;
+    for (int i0 = 0; i0 < a.n; i0 += kBook) {
+        const int i = i0 + threadIdx.x;
+        int total, one = 0;
+        if (i < a.n) {
+            const int row = a.a[i];
+            if (row >= 0 && row < a.n_rows) {
+                const int page = atomicExch(&a.table[row], -1);  // a row named twice is freed once
+                if (page >= 0 && page < a.n_pages) {
+                    a.owner[page] = -1;
+                    one = 1;
+                }
+            }
+        }
+        block_scan(one, total);
+        freed += total;
+    }
+    if (threadIdx.x == 0) a.result[0] = freed;
+}
+
+// ---- compacting --------------------------------------------------------------------------------
+// With n live pages, the live pages at n or past it move into the free pages below n, both lowest
+// first.  Sources and destinations are apart, so the copies need no order.
+__global__ void __launch_bounds__(kBook) cache_compact_kernel(const CacheArgs a) {
+    int live = 0;
+    for (int p0 = 0; p0 < a.n_pages; p0 += kBook) {
+        const int p = p0 + threadIdx.x;
+        int total;
+        block_scan(p < a.n_pages && a.owner[p] >= 0 ? 1 : 0, total);
+        live += total;
+    }
+    int holes = 0, moved = 0;
+    for (int p0 = 0; p0 < a.n_pages; p0 += kBook) {
+        const int p = p0 + threadIdx.x;
+        const bool in = p < a.n_pages, held = in && a.owner[p] >= 0;
+        const bool hole = in && p < live && !held, move = held && p >= live;
+        int th, tm;
+        const int hi = holes + block_scan(hole ? 1 : 0, th), mi = moved + block_scan(move ? 1 : 0, tm);
+        if (hole) a.moves[2 + 2 * hi] = p;
+        if (move) a.moves[1 + 2 * mi] = p;
+        if (in) a.result[p] = held ? p : -1;
+        holes += th;
+        moved += tm;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < moved; i += kBook) {  // holes == moved
+        const int from = a.moves[1 + 2 * i], to = a.moves[2 + 2 * i], row = a.owner[from];
+        a.owner[to] = row;
+        a.owner[from] = -1;
+        if (row < a.n_rows) a.table[row] = to;
+        a.result[from] = to;
+    }
+    if (threadIdx.x == 0) {
+        a.moves[0] = moved;
+        a.count[0] = live;
+    }
+}
+
+cudaError_t copy_moves(const CacheArgs& a, int most, cudaStream_t s) {
+    long long pieces = 0;
+    for (int k = 0; k < a.t.n; ++k) pieces += (a.t.bytes[k] + kPiece - 1) / kPiece;
+    if (pieces == 0 || most == 0) return cudaSuccess;
+    const long long want = pieces * most;
+    const unsigned grid = static_cast<unsigned>(want < 148 * 8 ? want : 148 * 8);  // 8 blocks of 256 threads an SM
+    cache_copy_kernel<<<grid, kCopy, 0, s>>>(a.t, a.moves, static_cast<int>(pieces));
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_copy(const CacheArgs& a, cudaStream_t s) {
+    cache_pairs_kernel<<<1, kBook, 0, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : copy_moves(a, a.n, s);
+}
+cudaError_t launch_cache_fork(const CacheArgs& a, cudaStream_t s) {
+    cache_fork_kernel<<<1, kBook, 0, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : copy_moves(a, a.n, s);
+}
+cudaError_t launch_cache_free(const CacheArgs& a, cudaStream_t s) {
+    cache_free_kernel<<<1, kBook, 0, s>>>(a);
+    return cudaGetLastError();
+}
+cudaError_t launch_cache_compact(const CacheArgs& a, cudaStream_t s) {
+    cache_compact_kernel<<<1, kBook, 0, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : copy_moves(a, a.n_pages / 2, s);
+}
+
+}  // namespace ttt

@@ -1,0 +1,596 @@
+// seq_api.cu -- the extern "C" entry points of the causal convolution, the selective scan and the
+// cache's page operations (declared in include/ttt.h).  Arguments are checked on the host before any
+// CUDA call; no device memory is allocated here.
+#include "api_util.h"
+#include "seq_internal.h"
+
+namespace {
+
+using ttt::aligned;
+using ttt::check_aliasing;
+using ttt::cuda_fail;
+using ttt::fail;
+using ttt::ok;
+using ttt::RowStride;
+using ttt::SeqShape;
+using ttt::Span;
+
+constexpr long long kMaxTokens = 1ll << 30;
+constexpr long long kMaxChannels = 1ll << 24;
+constexpr int kMaxStates = 64;
+constexpr int kSms = 148;  // B200
+
+int check_shape(int n_seq, long long L, int dim, int dtype) {
+    if (n_seq < 1 || n_seq > (1 << 24)) return fail(TTT_ERR_ARG, "n_seq must be in [1, 2^24] (got %d)", n_seq);
+    if (L < 0 || L >= kMaxTokens) return fail(TTT_ERR_ARG, "L must be in [0, 2^30) (got %lld)", L);
+    if (dim < 1 || dim > kMaxChannels) return fail(TTT_ERR_ARG, "the channels must be in [1, 2^24] (got %d)", dim);
+    if (dtype != TTT_F32 && dtype != TTT_BF16) return fail(TTT_ERR_ARG, "dtype must be TTT_F32 or TTT_BF16");
+    return TTT_OK;
+}
+
+size_t elem(int dtype) { return dtype == TTT_F32 ? 4 : 2; }
+
+// The strides of an operand: the caller's (batch, token), or those of contiguous rows of `width`.
+RowStride stride(const long long* strides, int i, long long L, long long width) {
+    return strides ? RowStride{strides[2 * i], strides[2 * i + 1]} : RowStride{L * width, width};
+}
+
+// Elements from the first to the last of n_seq x L rows of `width`.
+long long extent(RowStride r, bool packed, int n_seq, long long L, long long width) {
+    if (L == 0) return 0;
+    return (packed ? 0 : (n_seq - 1) * r.b) + (L - 1) * r.t + width;
+}
+
+// Input rows may repeat (stride 0); an output's must not touch one another.
+int check_stride(const char* name, RowStride r, bool packed, int n_seq, long long L, long long width, bool output) {
+    const long long big = 1ll << 50;
+    if (r.t < 0 || r.t > big || (!packed && (r.b < 0 || r.b > big)))
+        return fail(TTT_ERR_ARG, "%s: strides must be in [0, 2^50] (got %lld, %lld)", name, r.b, r.t);
+    if (!output) return TTT_OK;
+    const bool one_b = packed || n_seq == 1, one_t = L <= 1;
+    bool apart = (one_t || r.t >= width) && (one_b || r.b >= width);
+    if (apart && !one_b && !one_t) apart = r.b >= (L - 1) * r.t + width || r.t >= (n_seq - 1) * r.b + width;
+    if (!apart) return fail(TTT_ERR_ARG, "%s: the output's rows overlap (strides %lld, %lld)", name, r.b, r.t);
+    return TTT_OK;
+}
+
+int need(const char* name, const void* p, size_t align) {
+    if (!p) return fail(TTT_ERR_ARG, "%s must be non-null", name);
+    if (!aligned(p, align)) return fail(TTT_ERR_ALIGN, "%s must be %zu-byte aligned", name, align);
+    return TTT_OK;
+}
+int maybe(const char* name, const void* p, size_t align) { return p ? need(name, p, align) : TTT_OK; }
+
+#define TTT_TRY(x)           \
+    do {                     \
+        const int rc_ = (x); \
+        if (rc_) return rc_; \
+    } while (0)
+
+int check_pages(const int* pages, int n_pages, int n_seq) {
+    if (n_pages < 1) return fail(TTT_ERR_ARG, "n_pages must be >= 1 (got %d)", n_pages);
+    if (!pages && n_pages < n_seq)
+        return fail(TTT_ERR_ARG, "without pages, sequence b uses page b: n_pages (%d) must be >= n_seq (%d)", n_pages, n_seq);
+    return maybe("pages", pages, 4);
+}
+
+int check_conv(int n_seq, long long L, int D, int width, int dtype, unsigned int flags) {
+    TTT_TRY(check_shape(n_seq, L, D, dtype));
+    if (width < 1) return fail(TTT_ERR_ARG, "width must be >= 1 (got %d)", width);
+    if (width < 2 || width > 4) return fail(TTT_ERR_UNSUPPORTED, "only filter widths 2 to 4 are supported (got %d)", width);
+    if (flags & ~TTT_FLAG_SILU) return fail(TTT_ERR_ARG, "unknown flags 0x%x", flags);
+    return TTT_OK;
+}
+
+// Blocks of `span` tokens, at most 2^31 - 1.
+long long slot_count(bool packed, int n_seq, long long L, long long span) {
+    return packed ? L / span + n_seq : n_seq * (L > 0 ? (L + span - 1) / span : 1);
+}
+int check_grid(long long blocks) {
+    return blocks > 0x7fffffffll ? fail(TTT_ERR_ARG, "too many sequences, tokens or channels for one launch") : TTT_OK;
+}
+
+int check_scan(int n_seq, long long L, int dim, int groups, int N, int dtype, unsigned int flags) {
+    TTT_TRY(check_shape(n_seq, L, dim, dtype));
+    if (groups < 1 || dim % groups) return fail(TTT_ERR_ARG, "groups (%d) must divide dim (%d)", groups, dim);
+    if (N < 1) return fail(TTT_ERR_ARG, "d_state must be >= 1 (got %d)", N);
+    if (N > kMaxStates) return fail(TTT_ERR_UNSUPPORTED, "d_state up to %d is supported (got %d)", kMaxStates, N);
+    if (flags & ~TTT_FLAG_SOFTPLUS) return fail(TTT_ERR_ARG, "unknown flags 0x%x", flags);
+    const int ch = ttt::scan_channels(N), r = dim / groups;
+    return check_grid(slot_count(true, n_seq, L, 16) * groups * ((r + ch - 1) / ch));
+}
+
+// Into how many tokens a block's span is cut: whole sequences (split = false) where they fill the
+// GPU.
+struct Split {
+    bool on;
+    int span;
+    long long slots;
+};
+Split scan_split(int n_seq, long long L, long long longest, bool packed, int dim, int groups, int N) {
+    const int ch = ttt::scan_channels(N), r = dim / groups;
+    const long long tiles = static_cast<long long>(groups) * ((r + ch - 1) / ch);
+    const int whole = static_cast<int>((L + 16) / 16 * 16);  // past every token
+    Split s{false, whole, n_seq};
+    const long long blocks = tiles * n_seq, want = 4 * kSms;
+    if (blocks < 2 * kSms && longest >= 256) {
+        const long long total = packed ? L : n_seq * L;
+        long long span = (total * tiles + want - 1) / want;
+        span = (span < 64 ? 64 : span) / 16 * 16;
+        if (span * 2 <= longest) {
+            s.on = true;
+            s.span = static_cast<int>(span);
+            s.slots = slot_count(packed, n_seq, L, span);
+        }
+    }
+    return s;
+}
+size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+}  // namespace
+
+extern "C" {
+
+// ---- causal convolution ------------------------------------------------------------------------
+
+int ttt_causal_conv_forward(const void* x, const float* weight, const float* bias, const long long* strides,
+                            const int* cu_seqlens, const void* state_in, void* state_out, const int* pages,
+                            int n_pages, int n_seq, long long L, int dim, int width, int dtype, unsigned int flags,
+                            void* out, void* stream) {
+    TTT_TRY(check_conv(n_seq, L, dim, width, dtype, flags));
+    const size_t esz = elem(dtype);
+    const bool packed = cu_seqlens != nullptr;
+    TTT_TRY(need("weight", weight, 4));
+    TTT_TRY(maybe("bias", bias, 4));
+    TTT_TRY(maybe("cu_seqlens", cu_seqlens, 4));
+    TTT_TRY(maybe("state_in", state_in, esz));
+    TTT_TRY(maybe("state_out", state_out, esz));
+    if (L > 0) {
+        TTT_TRY(need("x", x, esz));
+        TTT_TRY(need("out", out, esz));
+    }
+    if (state_in || state_out) TTT_TRY(check_pages(pages, n_pages, n_seq));
+    const RowStride sx = stride(strides, 0, L, dim), so = stride(strides, 1, L, dim);
+    TTT_TRY(check_stride("x", sx, packed, n_seq, L, dim, false));
+    TTT_TRY(check_stride("out", so, packed, n_seq, L, dim, true));
+    TTT_TRY(check_grid(slot_count(true, n_seq, L, 8)));
+    const size_t st = static_cast<size_t>(n_pages) * (width - 1) * dim * esz;
+    const Span in[] = {{"x", x, extent(sx, packed, n_seq, L, dim) * esz}, {"weight", weight, static_cast<size_t>(dim) * width * 4},
+                       {"bias", bias, static_cast<size_t>(dim) * 4}, {"cu_seqlens", cu_seqlens, (n_seq + 1ull) * 4},
+                       {"state_in", state_in, st}, {"pages", pages, n_seq * 4ull}};
+    const Span outs[] = {{"out", out, extent(so, packed, n_seq, L, dim) * esz}, {"state_out", state_out, st}};
+    const int same_ok[1][2] = {{1, 4}};
+    TTT_TRY(check_aliasing(in, 6, outs, 2, same_ok, 1));
+    if (L == 0 && !state_out) return ok();
+    ttt::ConvArgs a{};
+    a.s = SeqShape{cu_seqlens, n_seq, L};
+    a.x = x; a.sx = sx; a.weight = weight; a.bias = bias; a.state_in = state_in; a.state_out = state_out;
+    a.pages = pages; a.n_pages = n_pages; a.D = dim; a.W = width; a.silu = (flags & TTT_FLAG_SILU) != 0;
+    a.out = out; a.so = so;
+    const cudaError_t e = ttt::launch_conv(a, dtype, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "ttt_causal_conv_forward launch");
+}
+
+int ttt_causal_conv_step(const void* x, const float* weight, const float* bias, const long long* strides, void* state,
+                         const int* pages, int n_pages, int n_seq, int dim, int width, int dtype, unsigned int flags,
+                         void* out, void* stream) {
+    TTT_TRY(check_conv(n_seq, 1, dim, width, dtype, flags));
+    const size_t esz = elem(dtype);
+    TTT_TRY(need("x", x, esz));
+    TTT_TRY(need("weight", weight, 4));
+    TTT_TRY(maybe("bias", bias, 4));
+    TTT_TRY(need("state", state, esz));
+    TTT_TRY(need("out", out, esz));
+    TTT_TRY(check_pages(pages, n_pages, n_seq));
+    const RowStride sx{strides ? strides[0] : dim, 0}, so{strides ? strides[1] : dim, 0};
+    TTT_TRY(check_stride("x", sx, false, n_seq, 1, dim, false));
+    TTT_TRY(check_stride("out", so, false, n_seq, 1, dim, true));
+    TTT_TRY(check_grid(static_cast<long long>(n_seq) * dim / 128 + 1));
+    const Span in[] = {{"x", x, extent(sx, false, n_seq, 1, dim) * esz}, {"weight", weight, static_cast<size_t>(dim) * width * 4},
+                       {"bias", bias, static_cast<size_t>(dim) * 4}, {"pages", pages, n_seq * 4ull}};
+    const Span outs[] = {{"out", out, extent(so, false, n_seq, 1, dim) * esz},
+                         {"state", state, static_cast<size_t>(n_pages) * (width - 1) * dim * esz}};
+    TTT_TRY(check_aliasing(in, 4, outs, 2));
+    ttt::ConvArgs a{};
+    a.s = SeqShape{nullptr, n_seq, 1};
+    a.x = x; a.sx = sx; a.weight = weight; a.bias = bias; a.state_out = state;
+    a.pages = pages; a.n_pages = n_pages; a.D = dim; a.W = width; a.silu = (flags & TTT_FLAG_SILU) != 0;
+    a.out = out; a.so = so;
+    const cudaError_t e = ttt::launch_conv_step(a, dtype, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "ttt_causal_conv_step launch");
+}
+
+long long ttt_causal_conv_backward_workspace_bytes(int n_seq, long long L, int dim, int width, int packed, int dtype) {
+    const int rc = check_conv(n_seq, L, dim, width, dtype, 0);
+    if (rc) return rc;
+    const int span = ttt::conv_bwd_span(n_seq, L, packed != 0, dim, dtype);
+    const long long slots = slot_count(packed != 0, n_seq, L, span);
+    ok();
+    return slots * (width + 1) * dim * 4;
+}
+
+int ttt_causal_conv_backward(const void* x, const float* weight, const float* bias, const long long* strides,
+                             const int* cu_seqlens, const void* state_in, int n_seq, long long L, int dim, int width,
+                             int dtype, unsigned int flags, const void* d_out, const void* d_state_out, void* dx,
+                             float* d_weight, float* d_bias, void* d_state_in, void* workspace,
+                             long long workspace_bytes, void* stream) {
+    TTT_TRY(check_conv(n_seq, L, dim, width, dtype, flags));
+    const size_t esz = elem(dtype);
+    const bool packed = cu_seqlens != nullptr;
+    TTT_TRY(need("weight", weight, 4));
+    TTT_TRY(maybe("bias", bias, 4));
+    TTT_TRY(maybe("cu_seqlens", cu_seqlens, 4));
+    TTT_TRY(maybe("state_in", state_in, esz));
+    TTT_TRY(maybe("d_state_out", d_state_out, esz));
+    TTT_TRY(maybe("d_state_in", d_state_in, esz));
+    TTT_TRY(need("d_weight", d_weight, 4));
+    TTT_TRY(maybe("d_bias", d_bias, 4));
+    if (L > 0) {
+        TTT_TRY(need("x", x, esz));
+        TTT_TRY(need("d_out", d_out, esz));
+        TTT_TRY(need("dx", dx, esz));
+    }
+    const RowStride sx = stride(strides, 0, L, dim), sd = stride(strides, 1, L, dim);
+    TTT_TRY(check_stride("x", sx, packed, n_seq, L, dim, false));
+    TTT_TRY(check_stride("d_out", sd, packed, n_seq, L, dim, false));
+    const long long bytes = ttt_causal_conv_backward_workspace_bytes(n_seq, L, dim, width, packed, dtype);
+    if (workspace_bytes < bytes) return fail(TTT_ERR_ARG, "workspace of %lld bytes; %lld are needed", workspace_bytes, bytes);
+    TTT_TRY(need("workspace", workspace, 256));
+    const int span = ttt::conv_bwd_span(n_seq, L, packed, dim, dtype);
+    const long long slots = slot_count(packed, n_seq, L, span);
+    TTT_TRY(check_grid(slots));
+    const size_t st = static_cast<size_t>(n_seq) * (width - 1) * dim * esz, wb = static_cast<size_t>(dim) * width * 4;
+    const size_t rows = static_cast<size_t>(packed ? L : n_seq * L) * dim * esz;
+    const Span in[] = {{"x", x, extent(sx, packed, n_seq, L, dim) * esz}, {"weight", weight, wb},
+                       {"bias", bias, static_cast<size_t>(dim) * 4}, {"cu_seqlens", cu_seqlens, (n_seq + 1ull) * 4},
+                       {"state_in", state_in, st}, {"d_out", d_out, extent(sd, packed, n_seq, L, dim) * esz},
+                       {"d_state_out", d_state_out, st}};
+    const Span outs[] = {{"dx", dx, rows}, {"d_weight", d_weight, wb}, {"d_bias", d_bias, static_cast<size_t>(dim) * 4},
+                         {"d_state_in", d_state_in, st}, {"workspace", workspace, static_cast<size_t>(bytes)}};
+    TTT_TRY(check_aliasing(in, 7, outs, 5));
+    ttt::ConvBwdArgs a{};
+    a.s = SeqShape{cu_seqlens, n_seq, L};
+    a.x = x; a.sx = sx; a.weight = weight; a.bias = bias; a.state_in = state_in; a.d_out = d_out; a.sd = sd;
+    a.d_state_out = d_state_out; a.D = dim; a.W = width; a.silu = (flags & TTT_FLAG_SILU) != 0;
+    a.dx = dx; a.d_state_in = d_state_in; a.d_weight = d_weight; a.d_bias = d_bias;
+    a.span = span; a.n_slots = static_cast<int>(slots); a.part = static_cast<float*>(workspace);
+    const cudaError_t e = ttt::launch_conv_bwd(a, dtype, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "ttt_causal_conv_backward launch");
+}
+
+// ---- selective scan ------------------------------------------------------------------------------
+
+long long ttt_selective_scan_ckpt_bytes(int n_seq, long long L, int dim, int d_state, int packed) {
+    const int rc = check_scan(n_seq, L, dim, 1, d_state, TTT_F32, 0);
+    if (rc) return rc;
+    ok();
+    return slot_count(packed != 0, n_seq, L, ttt::kScanChunk) * dim * d_state * 4;
+}
+
+long long ttt_selective_scan_workspace_bytes(int n_seq, long long L, long long max_seqlen, int packed, int dim,
+                                             int groups, int d_state) {
+    const int rc = check_scan(n_seq, L, dim, groups, d_state, TTT_F32, 0);
+    if (rc) return rc;
+    if (max_seqlen < 0) return fail(TTT_ERR_ARG, "max_seqlen must be >= 0 (got %lld)", max_seqlen);
+    const long long longest = packed && max_seqlen > 0 && max_seqlen < L ? max_seqlen : L;
+    const Split s = scan_split(n_seq, L, longest, packed != 0, dim, groups, d_state);
+    ok();
+    if (!s.on) return 0;
+    const size_t state = static_cast<size_t>(dim) * d_state * 4;
+    return static_cast<long long>(up256(s.slots * state) + up256(static_cast<size_t>(s.slots) * dim * 4) + up256(n_seq * state));
+}
+
+int ttt_selective_scan_forward(const void* u, const void* delta, const float* A, const void* B, const void* C,
+                               const float* D, const void* z, const float* delta_bias, const long long* strides,
+                               const int* cu_seqlens, long long max_seqlen, const float* state_in, float* state_out,
+                               const int* pages, int n_pages, int n_seq, long long L, int dim, int groups, int d_state,
+                               int dtype, unsigned int flags, void* out, float* ckpt, void* workspace,
+                               long long workspace_bytes, void* stream) {
+    TTT_TRY(check_scan(n_seq, L, dim, groups, d_state, dtype, flags));
+    const size_t esz = elem(dtype);
+    const bool packed = cu_seqlens != nullptr;
+    TTT_TRY(need("A", A, 16));
+    TTT_TRY(maybe("D", D, 4));
+    TTT_TRY(maybe("delta_bias", delta_bias, 4));
+    TTT_TRY(maybe("cu_seqlens", cu_seqlens, 4));
+    TTT_TRY(maybe("state_in", state_in, 16));
+    TTT_TRY(maybe("state_out", state_out, 16));
+    TTT_TRY(maybe("ckpt", ckpt, 16));
+    TTT_TRY(maybe("z", z, esz));
+    if (L > 0) {
+        TTT_TRY(need("u", u, esz));
+        TTT_TRY(need("delta", delta, esz));
+        TTT_TRY(need("B", B, esz));
+        TTT_TRY(need("C", C, esz));
+        TTT_TRY(need("out", out, esz));
+    }
+    if (state_in || state_out) TTT_TRY(check_pages(pages, n_pages, n_seq));
+    const long long bc = static_cast<long long>(groups) * d_state;
+    const RowStride su = stride(strides, 0, L, dim), sdt = stride(strides, 1, L, dim), sB = stride(strides, 2, L, bc),
+                    sC = stride(strides, 3, L, bc), sz = stride(strides, 4, L, dim), so = stride(strides, 5, L, dim);
+    TTT_TRY(check_stride("u", su, packed, n_seq, L, dim, false));
+    TTT_TRY(check_stride("delta", sdt, packed, n_seq, L, dim, false));
+    TTT_TRY(check_stride("B", sB, packed, n_seq, L, bc, false));
+    TTT_TRY(check_stride("C", sC, packed, n_seq, L, bc, false));
+    if (z) TTT_TRY(check_stride("z", sz, packed, n_seq, L, dim, false));
+    TTT_TRY(check_stride("out", so, packed, n_seq, L, dim, true));
+    const long long bytes = ttt_selective_scan_workspace_bytes(n_seq, L, max_seqlen, packed, dim, groups, d_state);
+    if (bytes < 0) return static_cast<int>(bytes);
+    if (bytes > 0) {
+        if (workspace_bytes < bytes) return fail(TTT_ERR_ARG, "workspace of %lld bytes; %lld are needed", workspace_bytes, bytes);
+        TTT_TRY(need("workspace", workspace, 256));
+    }
+    const size_t state = static_cast<size_t>(dim) * d_state * 4, st = n_pages * state;
+    auto ext = [&](RowStride r, long long w) { return extent(r, packed, n_seq, L, w) * esz; };
+    const Span in[] = {{"u", u, ext(su, dim)}, {"delta", delta, ext(sdt, dim)}, {"A", A, state}, {"B", B, ext(sB, bc)},
+                       {"C", C, ext(sC, bc)}, {"D", D, dim * 4ull}, {"z", z, z ? ext(sz, dim) : 0},
+                       {"delta_bias", delta_bias, dim * 4ull}, {"cu_seqlens", cu_seqlens, (n_seq + 1ull) * 4},
+                       {"state_in", state_in, st}, {"pages", pages, n_seq * 4ull}};
+    const Span outs[] = {{"out", out, ext(so, dim)}, {"state_out", state_out, st},
+                         {"ckpt", ckpt, slot_count(packed, n_seq, L, ttt::kScanChunk) * state},
+                         {"workspace", workspace, static_cast<size_t>(bytes)}};
+    const int same_ok[1][2] = {{1, 9}};
+    TTT_TRY(check_aliasing(in, 11, outs, 4, same_ok, 1));
+    if (L == 0 && !state_out) return ok();
+    const long long longest = packed && max_seqlen > 0 && max_seqlen < L ? max_seqlen : L;
+    const Split sp = scan_split(n_seq, L, longest, packed, dim, groups, d_state);
+    ttt::ScanArgs a{};
+    a.s = SeqShape{cu_seqlens, n_seq, L};
+    a.u = u; a.delta = delta; a.B = B; a.C = C; a.z = z;
+    a.su = su; a.sdt = sdt; a.sB = sB; a.sC = sC; a.sz = sz; a.so = so;
+    a.A = A; a.D = D; a.bias = delta_bias; a.dim = dim; a.groups = groups; a.N = d_state;
+    a.softplus = (flags & TTT_FLAG_SOFTPLUS) != 0;
+    a.state_in = state_in; a.state_out = state_out; a.pages = pages; a.n_pages = n_pages;
+    a.out = out; a.ckpt = ckpt; a.span = sp.span; a.n_slots = static_cast<int>(sp.slots); a.split = sp.on;
+    if (sp.on) {
+        char* w = static_cast<char*>(workspace);
+        a.seg_h = reinterpret_cast<float*>(w);
+        a.seg_dt = reinterpret_cast<float*>(w + up256(sp.slots * state));
+        a.seg_h0 = reinterpret_cast<float*>(w + up256(sp.slots * state) + up256(static_cast<size_t>(sp.slots) * dim * 4));
+    }
+    const cudaError_t e = ttt::launch_scan(a, dtype, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "ttt_selective_scan_forward launch");
+}
+
+int ttt_selective_scan_step(const void* u, const void* delta, const float* A, const void* B, const void* C,
+                            const float* D, const void* z, const float* delta_bias, const long long* strides,
+                            float* state, const int* pages, int n_pages, int n_seq, int dim, int groups, int d_state,
+                            int dtype, unsigned int flags, void* out, void* stream) {
+    TTT_TRY(check_scan(n_seq, 1, dim, groups, d_state, dtype, flags));
+    const size_t esz = elem(dtype);
+    TTT_TRY(need("u", u, esz));
+    TTT_TRY(need("delta", delta, esz));
+    TTT_TRY(need("A", A, 16));
+    TTT_TRY(need("B", B, esz));
+    TTT_TRY(need("C", C, esz));
+    TTT_TRY(maybe("D", D, 4));
+    TTT_TRY(maybe("z", z, esz));
+    TTT_TRY(maybe("delta_bias", delta_bias, 4));
+    TTT_TRY(need("state", state, 16));
+    TTT_TRY(need("out", out, esz));
+    TTT_TRY(check_pages(pages, n_pages, n_seq));
+    const long long bc = static_cast<long long>(groups) * d_state;
+    const long long own[6] = {dim, dim, bc, bc, dim, dim}, *sb = strides ? strides : own;
+    const char* names[6] = {"u", "delta", "B", "C", "z", "out"};
+    for (int i = 0; i < 6; ++i)
+        if (i != 4 || z)
+            TTT_TRY(check_stride(names[i], RowStride{sb[i], 0}, false, n_seq, 1, own[i], i == 5));
+    TTT_TRY(check_grid(static_cast<long long>(n_seq) * dim / 16 + 1));
+    auto ext = [&](int i) { return extent(RowStride{sb[i], 0}, false, n_seq, 1, own[i]) * esz; };
+    const size_t st = static_cast<size_t>(dim) * d_state * 4;
+    const Span in[] = {{"u", u, ext(0)}, {"delta", delta, ext(1)}, {"A", A, st}, {"B", B, ext(2)}, {"C", C, ext(3)},
+                       {"D", D, dim * 4ull}, {"z", z, z ? ext(4) : 0}, {"delta_bias", delta_bias, dim * 4ull},
+                       {"pages", pages, n_seq * 4ull}};
+    const Span outs[] = {{"out", out, ext(5)}, {"state", state, n_pages * st}};
+    TTT_TRY(check_aliasing(in, 9, outs, 2));
+    ttt::ScanStepArgs a{};
+    a.u = u; a.delta = delta; a.B = B; a.C = C; a.z = z;
+    a.su = sb[0]; a.sdt = sb[1]; a.sB = sb[2]; a.sC = sb[3]; a.sz = sb[4]; a.so = sb[5];
+    a.A = A; a.D = D; a.bias = delta_bias; a.n_seq = n_seq; a.dim = dim; a.groups = groups; a.N = d_state;
+    a.softplus = (flags & TTT_FLAG_SOFTPLUS) != 0;
+    a.state = state; a.pages = pages; a.n_pages = n_pages; a.out = out;
+    const cudaError_t e = ttt::launch_scan_step(a, dtype, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "ttt_selective_scan_step launch");
+}
+
+long long ttt_selective_scan_backward_workspace_bytes(int n_seq, long long L, int packed, int dim, int groups, int d_state) {
+    const int rc = check_scan(n_seq, L, dim, groups, d_state, TTT_F32, 0);
+    if (rc) return rc;
+    ok();
+    const int ch = ttt::scan_channels(d_state), tiles = (dim / groups + ch - 1) / ch;
+    const size_t rows = static_cast<size_t>(packed ? L : n_seq * L);
+    return static_cast<long long>(up256(tiles * rows * groups * 2 * d_state * 4) +
+                                  up256(static_cast<size_t>(n_seq) * dim * d_state * 4) +
+                                  up256(static_cast<size_t>(n_seq) * 2 * dim * 4));
+}
+
+int ttt_selective_scan_backward(const void* u, const void* delta, const float* A, const void* B, const void* C,
+                                const float* D, const void* z, const float* delta_bias, const long long* strides,
+                                const int* cu_seqlens, const float* ckpt, int n_seq, long long L, int dim, int groups,
+                                int d_state, int dtype, unsigned int flags, const void* d_out,
+                                const float* d_state_out, void* du, void* d_delta, float* dA, void* dB, void* dC,
+                                float* dD, void* dz, float* d_delta_bias, float* d_state_in, void* workspace,
+                                long long workspace_bytes, void* stream) {
+    TTT_TRY(check_scan(n_seq, L, dim, groups, d_state, dtype, flags));
+    const size_t esz = elem(dtype);
+    const bool packed = cu_seqlens != nullptr;
+    TTT_TRY(need("A", A, 16));
+    TTT_TRY(maybe("D", D, 4));
+    TTT_TRY(maybe("delta_bias", delta_bias, 4));
+    TTT_TRY(maybe("cu_seqlens", cu_seqlens, 4));
+    TTT_TRY(maybe("d_state_out", d_state_out, 16));
+    TTT_TRY(maybe("d_state_in", d_state_in, 16));
+    TTT_TRY(need("dA", dA, 4));
+    TTT_TRY(maybe("dD", dD, 4));
+    TTT_TRY(maybe("d_delta_bias", d_delta_bias, 4));
+    TTT_TRY(maybe("z", z, esz));
+    TTT_TRY(maybe("dz", dz, esz));
+    if ((z != nullptr) != (dz != nullptr) && L > 0) return fail(TTT_ERR_ARG, "z and dz must be given together");
+    if (L > 0) {
+        const void* ps[] = {u, delta, B, C, d_out, du, d_delta, dB, dC};
+        const char* names[] = {"u", "delta", "B", "C", "d_out", "du", "d_delta", "dB", "dC"};
+        for (int i = 0; i < 9; ++i) TTT_TRY(need(names[i], ps[i], esz));
+        TTT_TRY(need("ckpt", ckpt, 16));
+    }
+    const long long bc = static_cast<long long>(groups) * d_state;
+    const RowStride su = stride(strides, 0, L, dim), sdt = stride(strides, 1, L, dim), sB = stride(strides, 2, L, bc),
+                    sC = stride(strides, 3, L, bc), sz = stride(strides, 4, L, dim), sdo = stride(strides, 5, L, dim);
+    TTT_TRY(check_stride("u", su, packed, n_seq, L, dim, false));
+    TTT_TRY(check_stride("delta", sdt, packed, n_seq, L, dim, false));
+    TTT_TRY(check_stride("B", sB, packed, n_seq, L, bc, false));
+    TTT_TRY(check_stride("C", sC, packed, n_seq, L, bc, false));
+    if (z) TTT_TRY(check_stride("z", sz, packed, n_seq, L, dim, false));
+    TTT_TRY(check_stride("d_out", sdo, packed, n_seq, L, dim, false));
+    const long long bytes = ttt_selective_scan_backward_workspace_bytes(n_seq, L, packed, dim, groups, d_state);
+    if (workspace_bytes < bytes) return fail(TTT_ERR_ARG, "workspace of %lld bytes; %lld are needed", workspace_bytes, bytes);
+    TTT_TRY(need("workspace", workspace, 256));
+    const size_t state = static_cast<size_t>(dim) * d_state * 4, rows = static_cast<size_t>(packed ? L : n_seq * L);
+    auto ext = [&](RowStride r, long long w) { return extent(r, packed, n_seq, L, w) * esz; };
+    const Span in[] = {{"u", u, ext(su, dim)}, {"delta", delta, ext(sdt, dim)}, {"A", A, state}, {"B", B, ext(sB, bc)},
+                       {"C", C, ext(sC, bc)}, {"D", D, dim * 4ull}, {"z", z, z ? ext(sz, dim) : 0},
+                       {"delta_bias", delta_bias, dim * 4ull}, {"cu_seqlens", cu_seqlens, (n_seq + 1ull) * 4},
+                       {"ckpt", ckpt, slot_count(packed, n_seq, L, ttt::kScanChunk) * state},
+                       {"d_out", d_out, ext(sdo, dim)}, {"d_state_out", d_state_out, n_seq * state}};
+    const Span outs[] = {{"du", du, rows * dim * esz}, {"d_delta", d_delta, rows * dim * esz}, {"dA", dA, state},
+                         {"dB", dB, rows * bc * esz}, {"dC", dC, rows * bc * esz}, {"dD", dD, dim * 4ull},
+                         {"dz", dz, rows * dim * esz}, {"d_delta_bias", d_delta_bias, dim * 4ull},
+                         {"d_state_in", d_state_in, n_seq * state}, {"workspace", workspace, static_cast<size_t>(bytes)}};
+    TTT_TRY(check_aliasing(in, 12, outs, 10));
+    ttt::ScanBwdArgs a{};
+    a.s = SeqShape{cu_seqlens, n_seq, L};
+    a.u = u; a.delta = delta; a.B = B; a.C = C; a.z = z; a.d_out = d_out;
+    a.su = su; a.sdt = sdt; a.sB = sB; a.sC = sC; a.sz = sz; a.sdo = sdo;
+    a.A = A; a.D = D; a.bias = delta_bias; a.dim = dim; a.groups = groups; a.N = d_state;
+    a.softplus = (flags & TTT_FLAG_SOFTPLUS) != 0;
+    a.ckpt = ckpt; a.d_state_out = d_state_out;
+    a.du = du; a.ddelta = d_delta; a.dB = dB; a.dC = dC; a.dz = dz; a.dA = dA; a.dD = dD; a.dbias = d_delta_bias;
+    a.d_state_in = d_state_in;
+    const int ch = ttt::scan_channels(d_state);
+    a.tiles = (dim / groups + ch - 1) / ch;
+    char* w = static_cast<char*>(workspace);
+    a.part_bc = reinterpret_cast<float*>(w);
+    w += up256(static_cast<size_t>(a.tiles) * rows * bc * 2 * 4);
+    a.part_a = reinterpret_cast<float*>(w);
+    a.part_d = reinterpret_cast<float*>(w + up256(n_seq * state));
+    const cudaError_t e = ttt::launch_scan_bwd(a, dtype, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "ttt_selective_scan_backward launch");
+}
+
+// ---- pages of a cache ------------------------------------------------------------------------------
+
+namespace {
+
+int check_tensors(void* const* tensors, const long long* page_bytes, int n_tensors, int n_pages, ttt::CacheTensors* t) {
+    if (n_pages < 1) return fail(TTT_ERR_ARG, "n_pages must be >= 1 (got %d)", n_pages);
+    if (n_tensors < 0) return fail(TTT_ERR_ARG, "n_tensors must be >= 0 (got %d)", n_tensors);
+    if (n_tensors > ttt::kCacheMaxTensors)
+        return fail(TTT_ERR_UNSUPPORTED, "at most %d tensors a call (got %d)", ttt::kCacheMaxTensors, n_tensors);
+    if (n_tensors > 0 && (!tensors || !page_bytes)) return fail(TTT_ERR_ARG, "tensors and page_bytes must be non-null");
+    t->n = n_tensors;
+    long long all = 0;
+    for (int i = 0; i < n_tensors; ++i) {
+        if (!tensors[i]) return fail(TTT_ERR_ARG, "tensor %d is null", i);
+        if (page_bytes[i] < 1 || page_bytes[i] > (1ll << 40)) return fail(TTT_ERR_ARG, "page_bytes[%d] must be in [1, 2^40] (got %lld)", i, page_bytes[i]);
+        t->base[i] = static_cast<char*>(tensors[i]);
+        t->bytes[i] = page_bytes[i];
+        all += page_bytes[i];
+    }
+    if (all > (1ll << 42)) return fail(TTT_ERR_ARG, "the pages are too large (%lld bytes)", all);
+    return TTT_OK;
+}
+
+// No tensor may overlap another or one of `books`, nor the books one another.
+int check_apart(const ttt::CacheTensors& t, int n_pages, const Span* books, int n_books, const Span* reads, int n_reads) {
+    Span outs[ttt::kCacheMaxTensors + 4];
+    int n = 0;
+    for (int i = 0; i < t.n; ++i) outs[n++] = {"a page tensor", t.base[i], static_cast<size_t>(t.bytes[i]) * n_pages};
+    for (int i = 0; i < n_books; ++i) outs[n++] = books[i];
+    return check_aliasing(reads, n_reads, outs, n);
+}
+
+}  // namespace
+
+int ttt_cache_copy(void* const* tensors, const long long* page_bytes, int n_tensors, int n_pages, const int* src,
+                   const int* dst, int n, int* copied, int* workspace, void* stream) {
+    ttt::CacheArgs a{};
+    TTT_TRY(check_tensors(tensors, page_bytes, n_tensors, n_pages, &a.t));
+    if (n < 0 || n > n_pages) return fail(TTT_ERR_ARG, "n must be in [0, n_pages] (got %d of %d)", n, n_pages);
+    if (n == 0) return ok();
+    TTT_TRY(need("src", src, 4));
+    TTT_TRY(need("dst", dst, 4));
+    TTT_TRY(need("copied", copied, 4));
+    TTT_TRY(need("workspace", workspace, 4));
+    const Span reads[] = {{"src", src, n * 4ull}, {"dst", dst, n * 4ull}};
+    const Span books[] = {{"copied", copied, n * 4ull}, {"workspace", workspace, (1 + 2ull * n) * 4}};
+    TTT_TRY(check_apart(a.t, n_pages, books, 2, reads, 2));
+    a.n_pages = n_pages; a.n = n; a.a = src; a.b = dst; a.result = copied; a.moves = workspace;
+    const cudaError_t e = ttt::launch_cache_copy(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "ttt_cache_copy launch");
+}
+
+int ttt_cache_fork(void* const* tensors, const long long* page_bytes, int n_tensors, int n_pages, int* table,
+                   int n_rows, int* owner, const int* parents, const int* children, int n, int* pages, int* workspace,
+                   void* stream) {
+    ttt::CacheArgs a{};
+    TTT_TRY(check_tensors(tensors, page_bytes, n_tensors, n_pages, &a.t));
+    if (n_rows < 1) return fail(TTT_ERR_ARG, "n_rows must be >= 1 (got %d)", n_rows);
+    if (n < 0 || n > (1 << 24)) return fail(TTT_ERR_ARG, "n must be in [0, 2^24] (got %d)", n);
+    TTT_TRY(need("table", table, 4));
+    TTT_TRY(need("owner", owner, 4));
+    if (n == 0) return ok();
+    TTT_TRY(need("parents", parents, 4));
+    TTT_TRY(need("children", children, 4));
+    TTT_TRY(need("pages", pages, 4));
+    TTT_TRY(need("workspace", workspace, 4));
+    const Span reads[] = {{"parents", parents, n * 4ull}, {"children", children, n * 4ull}};
+    const Span books[] = {{"table", table, n_rows * 4ull}, {"owner", owner, n_pages * 4ull}, {"pages", pages, n * 4ull},
+                          {"workspace", workspace, (1 + 2ull * n) * 4}};
+    TTT_TRY(check_apart(a.t, n_pages, books, 4, reads, 2));
+    a.n_pages = n_pages; a.n_rows = n_rows; a.n = n; a.table = table; a.owner = owner; a.a = parents; a.b = children;
+    a.result = pages; a.moves = workspace;
+    const cudaError_t e = ttt::launch_cache_fork(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "ttt_cache_fork launch");
+}
+
+int ttt_cache_free(int* table, int n_rows, int* owner, int n_pages, const int* rows, int n, int* freed, void* stream) {
+    if (n_pages < 1 || n_rows < 1) return fail(TTT_ERR_ARG, "n_pages and n_rows must be >= 1 (got %d, %d)", n_pages, n_rows);
+    if (n < 0 || n > (1 << 24)) return fail(TTT_ERR_ARG, "n must be in [0, 2^24] (got %d)", n);
+    TTT_TRY(need("table", table, 4));
+    TTT_TRY(need("owner", owner, 4));
+    TTT_TRY(need("freed", freed, 4));
+    if (n > 0) TTT_TRY(need("rows", rows, 4));
+    const Span reads[] = {{"rows", rows, n * 4ull}};
+    const Span books[] = {{"table", table, n_rows * 4ull}, {"owner", owner, n_pages * 4ull}, {"freed", freed, 4}};
+    TTT_TRY(check_aliasing(reads, 1, books, 3));
+    ttt::CacheArgs a{};
+    a.n_pages = n_pages; a.n_rows = n_rows; a.n = n; a.table = table; a.owner = owner; a.a = rows; a.result = freed;
+    const cudaError_t e = ttt::launch_cache_free(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "ttt_cache_free launch");
+}
+
+int ttt_cache_compact(void* const* tensors, const long long* page_bytes, int n_tensors, int n_pages, int* table,
+                      int n_rows, int* owner, int* live, int* new_page, int* workspace, void* stream) {
+    ttt::CacheArgs a{};
+    TTT_TRY(check_tensors(tensors, page_bytes, n_tensors, n_pages, &a.t));
+    if (n_rows < 1) return fail(TTT_ERR_ARG, "n_rows must be >= 1 (got %d)", n_rows);
+    TTT_TRY(need("table", table, 4));
+    TTT_TRY(need("owner", owner, 4));
+    TTT_TRY(need("live", live, 4));
+    TTT_TRY(need("new_page", new_page, 4));
+    TTT_TRY(need("workspace", workspace, 4));
+    Span outs[ttt::kCacheMaxTensors + 5];
+    int k = 0;
+    for (int i = 0; i < a.t.n; ++i) outs[k++] = {"a page tensor", a.t.base[i], static_cast<size_t>(a.t.bytes[i]) * n_pages};
+    outs[k++] = {"table", table, n_rows * 4ull};
+    outs[k++] = {"owner", owner, n_pages * 4ull};
+    outs[k++] = {"live", live, 4};
+    outs[k++] = {"new_page", new_page, n_pages * 4ull};
+    outs[k++] = {"workspace", workspace, (2 + static_cast<size_t>(n_pages)) * 4};
+    TTT_TRY(check_aliasing(nullptr, 0, outs, k));
+    a.n_pages = n_pages; a.n_rows = n_rows; a.table = table; a.owner = owner; a.result = new_page; a.count = live;
+    a.moves = workspace;
+    const cudaError_t e = ttt::launch_cache_compact(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "ttt_cache_compact launch");
+}
+
+}  // extern "C"

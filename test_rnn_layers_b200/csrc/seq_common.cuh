@@ -1,0 +1,192 @@
+// seq_common.cuh -- what the causal convolution, the selective scan and their single-token steps
+// share: where a sequence's rows lie (a dense batch or packed sequences), pages of a state pool,
+// and the scalar functions.  Launch arguments are in seq_internal.h.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "seq_internal.h"
+#include "ttt_common.cuh"
+
+namespace ttt {
+
+// ---- sequences -------------------------------------------------------------------------------
+// A block's piece of work: piece `tile` (of `span` tokens) of sequence `b`, whose rows start at row
+// `t0` of batch row `row` and are `len` tokens long.  `slot` numbers the pieces: sequence b's
+// pieces have the slots slot_base(b) + 0, 1, ...
+struct Piece {
+    int b, tile, slot, len;
+    long long row, t0;
+};
+
+// Packed sequences: cu_seqlens entry i, held inside [0, T] whatever the array says.
+__device__ __forceinline__ long long cu_at(const int* cu, int i, long long T) {
+    long long v = cu[i];
+    return v < 0 ? 0 : (v > T ? T : v);
+}
+
+// Pieces of packed sequences are numbered without knowing the lengths on the host: sequence b owns
+// the slots from floor(cu[b] / span) + b on.  It needs ceil(len / span) of them (one if it is
+// empty), and floor(cu[b+1] / span) - floor(cu[b] / span) + 1 >= ceil(len / span), so no two
+// sequences share a slot and floor(T / span) + n_seq slots hold all of them.
+__device__ __forceinline__ long long slot_base(const int* cu, int b, long long T, int span) {
+    return cu_at(cu, b, T) / span + b;
+}
+
+// The piece of slot `slot`.  False if the slot holds nothing (a sequence's spare slot).  An empty
+// sequence has one piece, of no tokens.
+__device__ __forceinline__ bool find_piece(const SeqShape& s, int slot, int span, Piece& p) {
+    p.slot = slot;
+    if (!s.cu) {
+        const int per = s.L > 0 ? static_cast<int>((s.L + span - 1) / span) : 1;
+        p.b = slot / per;
+        p.tile = slot - p.b * per;
+        p.row = p.b;
+        p.t0 = 0;
+        p.len = static_cast<int>(s.L);
+        return true;
+    }
+    int lo = 0, hi = s.n_seq - 1;  // the last b with slot_base(b) <= slot
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (slot_base(s.cu, mid, s.L, span) <= slot) lo = mid; else hi = mid - 1;
+    }
+    p.b = lo;
+    p.tile = slot - static_cast<int>(slot_base(s.cu, lo, s.L, span));
+    p.row = 0;
+    p.t0 = cu_at(s.cu, lo, s.L);
+    const long long end = cu_at(s.cu, lo + 1, s.L);
+    p.len = end > p.t0 ? static_cast<int>(end - p.t0) : 0;
+    return p.tile == 0 || (p.tile > 0 && static_cast<long long>(p.tile) * span < p.len);
+}
+
+// Page of sequence b, or -1 if it has none (or an index outside the pool).
+__device__ __forceinline__ int page_of(const int* pages, int n_pages, int b) {
+    const int p = pages ? pages[b] : b;
+    return p >= 0 && p < n_pages ? p : -1;
+}
+
+// ---- element vectors: VEC consecutive channels as floats -------------------------------------
+template <int VEC>
+__device__ __forceinline__ void load_vec(const float* p, float (&v)[VEC]) {
+    if constexpr (VEC == 4) {
+        const float4 t = *reinterpret_cast<const float4*>(p);
+        v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+    } else if constexpr (VEC == 2) {
+        const float2 t = *reinterpret_cast<const float2*>(p);
+        v[0] = t.x; v[1] = t.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = p[i];
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&v)[VEC]) {
+    if constexpr (VEC == 8) {
+        const uint4 t = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack_bf16x2(w[i]);
+            v[2 * i] = f.x; v[2 * i + 1] = f.y;
+        }
+    } else if constexpr (VEC == 4) {
+        const uint2 t = *reinterpret_cast<const uint2*>(p);
+        const float2 f = unpack_bf16x2(t.x), g = unpack_bf16x2(t.y);
+        v[0] = f.x; v[1] = f.y; v[2] = g.x; v[3] = g.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = __bfloat162float(p[i]);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void store_vec(float* p, const float (&v)[VEC]) {
+    if constexpr (VEC == 4) {
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else if constexpr (VEC == 2) {
+        *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) p[i] = v[i];
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&v)[VEC]) {
+    if constexpr (VEC == 8) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    } else if constexpr (VEC == 4) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) p[i] = __float2bfloat16_rn(v[i]);
+    }
+}
+
+// ---- scalar functions ------------------------------------------------------------------------
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 2^x for a decay factor.  A state that decays by 2^x a token remembers about 1 / |x| tokens, and a
+// relative bias of the factor adds up over all of them, so what has to be small is the error of
+// 2^x - 1 relative to x.  The hardware's exponential is low by 5e-8 on average for |x| > 0.5 and by
+// 6e-9 .. 3e-8 near zero (measured), which is 8e-6 of the state for x around -0.001.  For
+// |x| < 1/8 a polynomial 1 + x q(x) is used instead, with q the cubic of least relative error to
+// (2^x - 1) / x there (6e-8, a least-maximum fit); the hardware's exponential is within 4e-7 of the
+// state beyond.  Infinities and NaN go through the hardware's exponential.
+__device__ __forceinline__ float decay2(float x) {
+    const float e = ex2_approx(x);
+    float q = fmaf(x, 0.009618128649890423f, 0.05552494153380394f);
+    q = fmaf(x, q, 0.24022653698921204f);
+    q = fmaf(x, q, 0.6931471805599453f);
+    return fabsf(x) < 0.125f ? fmaf(x, q, 1.0f) : e;
+}
+
+// 1 / (1 + e^-x)
+__device__ __forceinline__ float sigmoid_f(float x) { return rcp_approx(1.0f + ex2_approx(-x * kLog2e)); }
+// x / (1 + e^-x)
+__device__ __forceinline__ float silu_f(float x) { return x * sigmoid_f(x); }
+// d silu / dx, given sigmoid(x)
+__device__ __forceinline__ float silu_grad_f(float x, float sg) { return sg * fmaf(x, 1.0f - sg, 1.0f); }
+
+// log(1 + e^x) = max(x, 0) + log1p(e), e = e^-|x| in [0, 1].  With s = e / (2 + e) <= 1/3,
+// log1p(e) = 2 artanh(s) = s R(s^2); R is fitted to 4e-9 (least maximum of the relative error), so
+// the small steps e^x of a very negative x keep their relative accuracy.
+__device__ __forceinline__ float softplus_f(float x) {
+    const float e = expf(-fabsf(x));
+    const float s = __fdividef(e, 2.0f + e), w = s * s;
+    float r = fmaf(w, 0.2817833423614502f, 0.27960601449012756f);
+    r = fmaf(w, r, 0.40024909377098083f);
+    r = fmaf(w, r, 0.6666631698608398f);
+    r = fmaf(w, r, 2.0f);
+    return fmaf(s, r, fmaxf(x, 0.0f));  // a NaN comes through s
+}
+
+// Sums over the lanes CPW, 2 CPW, ... apart (P of them, lane / CPW = q), of P values per lane: on
+// return lane q holds the sum of value q.  P - 1 shuffles instead of P log2 P.
+template <int P, int CPW>
+__device__ __forceinline__ float reduce_across(float (&v)[P], int q) {
+#pragma unroll
+    for (int w = P / 2; w >= 1; w /= 2) {
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+            const float send = (q & w) ? v[i] : v[i + w], keep = (q & w) ? v[i + w] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, w * CPW);
+        }
+    }
+    return v[0];
+}
+
+}  // namespace ttt

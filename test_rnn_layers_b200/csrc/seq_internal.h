@@ -1,0 +1,142 @@
+// seq_internal.h -- launch arguments and launchers of the causal convolution, the selective scan and
+// the cache's page operations, shared by seq_api.cu and the kernels.  Not part of the public ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace ttt {
+
+// Where the rows of the sequences lie.  cu == nullptr: a dense batch of n_seq sequences of L tokens,
+// row t of sequence b at b * batch stride + t * token stride.  Otherwise packed: L rows in all,
+// sequence b the rows cu[b] .. cu[b+1] - 1 (batch strides unused).
+struct SeqShape {
+    const int* cu;
+    int n_seq;
+    long long L;
+};
+
+// Element strides of a tensor's batch rows and tokens (channels are contiguous).
+struct RowStride {
+    long long b, t;
+};
+
+struct ConvArgs {
+    SeqShape s;
+    const void* x;
+    RowStride sx;
+    const float* weight;      // [D][W]
+    const float* bias;        // [D] or nullptr
+    const void* state_in;     // [n_pages][W-1][D] or nullptr (zeros)
+    void* state_out;          // [n_pages][W-1][D] or nullptr
+    const int* pages;         // [n_seq] or nullptr (page b)
+    int n_pages;
+    int D, W, silu;
+    void* out;
+    RowStride so;
+    int span;                 // tokens per block
+};
+
+struct ConvBwdArgs {
+    SeqShape s;
+    const void* x;
+    RowStride sx;
+    const float* weight;
+    const float* bias;
+    const void* state_in;     // [n_seq][W-1][D] or nullptr
+    const void* d_out;
+    RowStride sd;
+    const void* d_state_out;  // [n_seq][W-1][D] or nullptr
+    int D, W, silu;
+    void* dx;                 // rows laid out contiguously: [n_seq][L][D], or [L][D] packed
+    void* d_state_in;         // [n_seq][W-1][D] or nullptr
+    float* d_weight;          // [D][W]
+    float* d_bias;            // [D] or nullptr
+    int span;
+    int n_slots;
+    float* part;              // [n_slots][W + 1][D]: each block's shares of d_weight and d_bias
+};
+
+struct ScanArgs {
+    SeqShape s;
+    const void *u, *delta, *B, *C, *z;
+    RowStride su, sdt, sB, sC, sz, so;
+    const float *A, *D, *bias;   // [dim][N], [dim] or nullptr, [dim] or nullptr
+    int dim, groups, N, softplus;
+    const float* state_in;       // [n_pages][dim][N] or nullptr
+    float* state_out;            // [n_pages][dim][N] or nullptr
+    const int* pages;
+    int n_pages;
+    void* out;
+    float* ckpt;                 // [chunk][dim][N] or nullptr: the state before every kScanChunk-th token
+    int span;                    // tokens per block (a multiple of 16); the whole sequence if split == 0
+    int n_slots;
+    int split;                   // 1: sequences are cut into spans (two launches)
+    float* seg_h;                // [n_slots][dim][N]: each span's own end state
+    float* seg_dt;               // [n_slots][dim]: each span's sum of delta
+    float* seg_h0;               // [n_seq][dim][N]: the start states
+};
+constexpr int kScanChunk = 8;    // tokens between the states a training forward keeps
+
+struct ScanStepArgs {
+    const void *u, *delta, *B, *C, *z;
+    long long su, sdt, sB, sC, sz, so;  // batch strides
+    const float *A, *D, *bias;
+    int n_seq, dim, groups, N, softplus;
+    float* state;
+    const int* pages;
+    int n_pages;
+    void* out;
+};
+
+struct ScanBwdArgs {
+    SeqShape s;
+    const void *u, *delta, *B, *C, *z, *d_out;
+    RowStride su, sdt, sB, sC, sz, sdo;
+    const float *A, *D, *bias;
+    int dim, groups, N, softplus;
+    const float* ckpt;
+    const float* d_state_out;    // [n_seq][dim][N] or nullptr
+    void *du, *ddelta, *dB, *dC, *dz;   // contiguous rows
+    float *dA, *dD, *dbias;
+    float* d_state_in;           // [n_seq][dim][N] or nullptr
+    int tiles;                   // channel tiles per group
+    float* part_bc;              // [tiles][rows][groups][2][N]
+    float* part_a;               // [n_seq][dim][N]
+    float* part_d;               // [n_seq][2][dim]: d D, d bias
+};
+
+constexpr int kCacheMaxTensors = 64;
+struct CacheTensors {
+    int n;
+    char* base[kCacheMaxTensors];
+    long long bytes[kCacheMaxTensors];   // per page
+};
+struct CacheArgs {
+    CacheTensors t;
+    int n_pages, n_rows, n;
+    int* table;                  // [n_rows]
+    int* owner;                  // [n_pages]
+    const int* a;                // fork: parents; copy: sources; free: rows
+    const int* b;                // fork: children; copy: destinations
+    int* result;                 // fork: [n] pages; copy: [n]; compact: [n_pages]; free: [1]
+    int* count;                  // compact: [1]
+    int* moves;                  // [1 + 2 * most moves]: the pairs to copy
+};
+
+cudaError_t launch_conv(const ConvArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_conv_step(const ConvArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_conv_bwd(const ConvBwdArgs& a, int dtype, cudaStream_t s);
+int conv_bwd_span(int n_seq, long long L, bool packed, int D, int dtype);
+
+int scan_channels(int N);        // channels per block of the scan kernels
+cudaError_t launch_scan(const ScanArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_scan_step(const ScanStepArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_scan_bwd(const ScanBwdArgs& a, int dtype, cudaStream_t s);
+
+cudaError_t launch_cache_copy(const CacheArgs& a, cudaStream_t s);
+cudaError_t launch_cache_fork(const CacheArgs& a, cudaStream_t s);
+cudaError_t launch_cache_free(const CacheArgs& a, cudaStream_t s);
+cudaError_t launch_cache_compact(const CacheArgs& a, cudaStream_t s);
+
+}  // namespace ttt

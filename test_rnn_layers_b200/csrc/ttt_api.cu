@@ -10,16 +10,14 @@
 #include <string>
 
 #include "../../include/ttt.h"
+#include "api_util.h"
 #include "ttt_internal.h"
 
+// The last-error message of this host thread (api_util.h).
+namespace ttt {
 namespace {
-
 thread_local std::string g_last_error;
-std::atomic<long long> g_wait_limit{0};
-constexpr long long kDefaultWaitPolls = 1ll << 24;
-constexpr int kD = 64;
-constexpr int kHidden = 256;
-
+}
 int fail(int code, const char* fmt, ...) {
     char buf[512];
     va_list ap;
@@ -29,47 +27,25 @@ int fail(int code, const char* fmt, ...) {
     g_last_error = buf;
     return code;
 }
-
 int ok() {
     g_last_error.clear();
     return TTT_OK;
 }
+}  // namespace ttt
 
-bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+namespace {
 
-// A byte range [p, p + n) of one argument, for the overlap checks.
-struct Span {
-    const char* name;
-    const void* p;
-    size_t n;
-};
+using ttt::aligned;
+using ttt::check_aliasing;
+using ttt::cuda_fail;
+using ttt::fail;
+using ttt::ok;
+using ttt::Span;
 
-bool overlaps(const Span& x, const Span& y) {
-    if (!x.p || !y.p || x.n == 0 || y.n == 0) return false;
-    auto a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
-    return a < b + y.n && b < a + x.n;
-}
-
-// outputs must not overlap inputs or each other; `same_ok` lists (output, input) index pairs
-// allowed to be the SAME buffer (identical pointer and size: an in-place state update).
-int check_aliasing(const Span* in, int nin, const Span* out, int nout,
-                   const int (*same_ok)[2] = nullptr, int nsame = 0) {
-    for (int o = 0; o < nout; ++o) {
-        for (int i = 0; i < nin; ++i) {
-            if (!overlaps(out[o], in[i])) continue;
-            bool allowed = false;
-            for (int k = 0; k < nsame; ++k)
-                if (same_ok[k][0] == o && same_ok[k][1] == i && out[o].p == in[i].p && out[o].n == in[i].n)
-                    allowed = true;
-            if (!allowed)
-                return fail(TTT_ERR_ALIAS, "output %s overlaps input %s", out[o].name, in[i].name);
-        }
-        for (int p = o + 1; p < nout; ++p)
-            if (overlaps(out[o], out[p]))
-                return fail(TTT_ERR_ALIAS, "outputs %s and %s overlap", out[o].name, out[p].name);
-    }
-    return TTT_OK;
-}
+std::atomic<long long> g_wait_limit{0};
+constexpr long long kDefaultWaitPolls = 1ll << 24;
+constexpr int kD = 64;
+constexpr int kHidden = 256;
 
 unsigned int* status_word();  // device address of the status word of the current device
 
@@ -132,10 +108,6 @@ void set_act_strides(Args& a, int H, long long L, bool tok_major) {
     a.act_h = tok_major ? kD : L * kD;
     a.act_t = tok_major ? hd : kD;
     a.tok_major = tok_major ? 1 : 0;
-}
-
-int cuda_fail(cudaError_t e, const char* what) {
-    return fail(TTT_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
 // Common checks of the prefill entry points.
@@ -314,7 +286,7 @@ const char* ttt_error_string(int code) {
     }
 }
 
-const char* ttt_last_error_message(void) { return g_last_error.c_str(); }
+const char* ttt_last_error_message(void) { return ttt::g_last_error.c_str(); }
 
 int ttt_set_wait_limit(long long polls) {
     g_wait_limit.store(polls);
