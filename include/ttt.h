@@ -64,6 +64,9 @@ extern "C" {
 #define TTT_FLAG_SOFTPLUS 8u
 /* ttt_causal_conv_*: the output passes through silu. */
 #define TTT_FLAG_SILU 16u
+/* ttt_causal_conv_* and ttt_selective_scan_* with cu_seqlens: rows outside every sequence are written
+ * as zeros in the outputs instead of being left as they were. */
+#define TTT_FLAG_ZERO_REST 32u
 
 /* Bits of the device status word */
 #define TTT_STATUS_TIMEOUT 1u /* a kernel gave up on a bounded wait and returned early */
@@ -527,16 +530,16 @@ int ttt_linear_backward_ckpt(const void* XQ, const void* XK, const void* XV, con
  *  - Activations are rows of channels: a dense batch [n_seq, L, dim], or, with cu_seqlens, packed
  *    sequences [L, dim] of which sequence b owns the rows cu_seqlens[b] .. cu_seqlens[b+1] - 1
  *    (int32 [n_seq + 1] on the device, not decreasing, within [0, L]; entries outside [0, L] are held
- *    inside it, so a bad array cannot make a call read or write out of bounds).  Rows past the last
- *    sequence are neither read nor written.  Sequences may be empty, L may be 0.
+ *    inside it, so a bad array cannot make a call read or write out of bounds).  Rows before the first
+ *    and past the last sequence are not read, and written (as zeros) with TTT_FLAG_ZERO_REST only.
+ *    Sequences may be empty, L may be 0.
  *  - strides: NULL for contiguous rows, or a HOST array of element strides, (batch, token) for each
  *    operand in the order that the call names; channels are contiguous.  Input strides may be 0 (a
  *    broadcast row); an output's rows must not overlap.  With cu_seqlens the batch strides are not
  *    used.  Rows need no alignment beyond their element's; 16-byte aligned rows are read faster.
  *  - States lie in pages of a pool, page p of [n_pages, ...] at p; sequence b uses page pages[b]
  *    (int32 [n_seq] on the device), or page b if pages is NULL.  A sequence whose entry is negative or
- *    >= n_pages has no state: prompts start from zeros and keep nothing, steps leave its row of out as
- *    it was.  The pages of one call have to differ from each other: if two sequences name one page,
+ *    >= n_pages has no state: prompts start from zeros and keep nothing, steps give a row of zeros.  The pages of one call have to differ from each other: if two sequences name one page,
  *    that page and the two sequences' results are unspecified (nothing else is touched).
  *  - dtype is that of the activations and of the convolution's state; weights, biases, A, D and the
  *    scan's state are float32.  Sums, states and the gradients of the parameters are held in float32;
@@ -554,7 +557,7 @@ int ttt_linear_backward_ckpt(const void* XQ, const void* XK, const void* XV, con
  *                sequence's first (oldest first); zeros if NULL.
  *   state_out    the same pool shape or NULL: receives the last width - 1 inputs (for the next part
  *                of the sequence or ttt_causal_conv_step).  May be state_in itself.
- *   flags        TTT_FLAG_SILU (act = silu) or 0 (identity).
+ *   flags        TTT_FLAG_SILU (act = silu) or 0 (identity), and TTT_FLAG_ZERO_REST.
  *   out          as x, dtype.
  */
 int ttt_causal_conv_forward(const void* x, const float* weight, const float* bias, const long long* strides,

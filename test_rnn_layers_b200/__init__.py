@@ -31,6 +31,7 @@ TTT_FLAG_TOKEN_MAJOR = 2
 TTT_FLAG_ROPE_HALF_SPLIT = 4
 TTT_FLAG_SOFTPLUS = 8
 TTT_FLAG_SILU = 16
+TTT_FLAG_ZERO_REST = 32
 TTT_STATUS_TIMEOUT = 1
 TTT_STATIC_SCRATCH_BYTES = 33554432
 
@@ -600,66 +601,107 @@ def ttt_linear_backward(XQ, XK, XV, lr, W0, b0, ln_w, ln_b, d_out, dW_last=None,
 
 class _On:
     """The device and stream of a call: its tensors' device is made current, and what the call
-    allocates belongs to the stream it runs on."""
+    allocates belongs to the stream it runs on.  (Decode steps are a few microseconds of GPU work, so
+    the checks below are written to cost the host little.)"""
+
+    __slots__ = ("index", "device", "handle", "_ctx")
 
     def __init__(self, t, stream):
         if not isinstance(t, torch.Tensor):
             raise TypeError("the first argument must be a torch.Tensor")
-        if not t.is_cuda:
+        self.index = t.get_device()
+        if self.index < 0:
             raise ValueError("the tensors must be CUDA tensors (there is no CPU path)")
         self.device = t.device
-        self.stream = torch.cuda.current_stream(t.device) if stream is None else stream
-        if self.stream.device != t.device:
-            raise ValueError(f"the stream is on {self.stream.device}, the tensors on {t.device}")
-        self._ctx = torch.cuda.stream(self.stream)
+        if stream is None:
+            self.handle = torch._C._cuda_getCurrentRawStream(self.index)
+            self._ctx = None if torch._C._cuda_getDevice() == self.index else torch.cuda.device(self.index)
+        else:
+            if stream.device != self.device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
+            self.handle = stream.cuda_stream
+            self._ctx = torch.cuda.stream(stream)
 
     def __enter__(self):
-        self._ctx.__enter__()
+        if self._ctx is not None:
+            self._ctx.__enter__()
         return self
 
     def __exit__(self, *exc):
-        return self._ctx.__exit__(*exc)
+        if self._ctx is not None:
+            return self._ctx.__exit__(*exc)
 
-    def need(self, t, name, dtype=None, shape=None):
-        _need(t, name, dtype, shape)
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, the first argument on {self.device}")
-        return t
-
-    def maybe(self, t, name, dtype=None, shape=None):
-        return None if t is None else self.need(t, name, dtype, shape)
-
-    def rows(self, t, name, dtype, shape, inner: int = 1):
-        """t's (batch, token) element strides; its last `inner` dimensions must be contiguous."""
+    def ptr(self, t, name, dtype=None, shape=None):
+        """Address of a contiguous tensor (None: no tensor)."""
+        if t is None:
+            return None
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if t.device != self.device:
+        if t.get_device() != self.index:
             raise ValueError(f"{name} is on {t.device}, the first argument on {self.device}")
-        if t.dtype != dtype:
+        if dtype is not None and t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if tuple(t.shape) != tuple(shape):
+        if shape is not None and t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        want = 1
-        for k in range(1, inner + 1):
-            if t.shape[-k] > 1 and t.stride(-k) != want:
-                raise ValueError(f"{name}: its channels must be contiguous, got strides {tuple(t.stride())}")
-            want *= t.shape[-k]
-        lead = t.stride()[:-inner]
-        return (0, *lead) if len(lead) == 1 else lead
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def need(self, t, name, dtype=None, shape=None):
+        if t is None:
+            raise TypeError(f"{name} must be a torch.Tensor")
+        return self.ptr(t, name, dtype, shape)
 
     def workspace(self, nbytes: int, given=None):
         if given is not None:
-            return self.need(given, "workspace", torch.uint8)
+            self.need(given, "workspace", torch.uint8)
+            return given
         return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
 
-    @property
-    def handle(self):
-        return ctypes.c_void_p(self.stream.cuda_stream)
 
+class _Rows:
+    """The operands of a call that are rows of channels: their addresses, and their (batch, token) element
+    strides unless all of them are contiguous."""
 
-def _strides(*pairs):
-    flat = [int(s) for p in pairs for s in p]
-    return (ctypes.c_longlong * len(flat))(*flat)
+    __slots__ = ("on", "dtype", "views")
+
+    def __init__(self, on, dtype):
+        self.on, self.dtype, self.views = on, dtype, []
+
+    def __call__(self, t, name, shape, inner: int = 1):
+        """The address of t (None: no tensor); its last `inner` dimensions must be contiguous."""
+        if t is None:
+            self.views.append(None)
+            return None
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.get_device() != self.on.index:
+            raise ValueError(f"{name} is on {t.device}, the first argument on {self.on.device}")
+        if t.dtype != self.dtype:
+            raise TypeError(f"{name} must be {self.dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.is_contiguous():
+            self.views.append(None)
+        else:
+            want = 1
+            for k in range(1, inner + 1):
+                if t.shape[-k] > 1 and t.stride(-k) != want:
+                    raise ValueError(f"{name}: its channels must be contiguous, got strides {tuple(t.stride())}")
+                want *= t.shape[-k]
+            self.views.append(t.stride()[:-inner])
+        return t.data_ptr()
+
+    def strides(self, *contiguous):
+        """The ABI's strides: None if every operand is contiguous, else (batch, token) of each (`contiguous`
+        holds what those are for the operands that are)."""
+        if not any(v is not None for v in self.views):
+            return None
+        flat = []
+        for v, c in zip(self.views, contiguous):
+            v = c if v is None else v
+            flat += [0] * (len(c) - len(v)) + [int(x) for x in v]
+        return (ctypes.c_longlong * len(flat))(*flat)
 
 
 def _bytes(n) -> int:
@@ -681,18 +723,12 @@ def _seq_sizes(x, name, cu_seqlens):
     return cu_seqlens.numel() - 1, x.shape[0], (x.shape[0],)
 
 
-def _new_rows(shape, dtype, device, cu_seqlens):
-    """An output: rows past the last packed sequence are not written, so they start as zeros."""
-    return torch.empty(shape, dtype=dtype, device=device) if cu_seqlens is None else torch.zeros(shape, dtype=dtype, device=device)
-
-
 def _pool(on, pages, n_seq, *pools):
-    """Pages of the state pools given (each None or [n_pages, ...])."""
-    on.maybe(pages, "pages", torch.int32, (n_seq,))
+    """(address of pages, n_pages) for the state pools given (each None or [n_pages, ...])."""
     sizes = {p.shape[0] for p in pools if p is not None}
     if len(sizes) > 1:
         raise ValueError("state_in and state_out must have the same number of pages")
-    return sizes.pop() if sizes else 0
+    return on.ptr(pages, "pages", torch.int32, (n_seq,)), sizes.pop() if sizes else 0
 
 
 def ttt_causal_conv_forward(x, weight, bias=None, silu: bool = True, state_in=None, state_out=None, pages=None,
@@ -701,51 +737,45 @@ def ttt_causal_conv_forward(x, weight, bias=None, silu: bool = True, state_in=No
     dim], or packed rows [L, dim] with cu_seqlens (int32 [n_seq + 1]); weight [dim, width], bias [dim]
     float32.  state_in / state_out: pools [n_pages, width - 1, dim] in x's dtype holding the inputs
     before / after each sequence, in the pages named by `pages` (int32 [n_seq], default page b).
-    x may be a strided view with contiguous channels.  Returns out (see include/ttt.h)."""
+    x may be a strided view with contiguous channels.  Rows of a given `out` outside every sequence stay as
+    they were; in one allocated here they are zero.  Returns out (see include/ttt.h)."""
     with _On(x, stream) as on:
         n_seq, L, lead = _seq_sizes(x, "x", cu_seqlens)
-        dim = x.shape[-1]
-        sx = on.rows(x, "x", x.dtype, (*lead, dim))
-        if weight.dim() != 2:
-            raise ValueError("weight must be [dim, width]")
-        width = weight.shape[1]
-        on.need(weight, "weight", torch.float32, (dim, width))
-        on.maybe(bias, "bias", torch.float32, (dim,))
-        on.maybe(cu_seqlens, "cu_seqlens", torch.int32)
-        n_pages = _pool(on, pages, n_seq, state_in, state_out)
-        for n, t in (("state_in", state_in), ("state_out", state_out)):
-            on.maybe(t, n, x.dtype, (n_pages, width - 1, dim))
+        dim, width, dt = x.shape[-1], weight.shape[-1], x.dtype
+        flags = TTT_FLAG_SILU if silu else 0
         if out is None:
-            out = _new_rows(x.shape, x.dtype, on.device, cu_seqlens)
-        so = on.rows(out, "out", x.dtype, x.shape)
-        _check(lib().ttt_causal_conv_forward(_ptr(x), _ptr(weight), _ptr(bias), _strides(sx, so), _ptr(cu_seqlens),
-                                             _ptr(state_in), _ptr(state_out), _ptr(pages), n_pages, n_seq, L, dim,
-                                             width, _dtype_code(x), TTT_FLAG_SILU if silu else 0, _ptr(out), on.handle))
+            out = torch.empty(x.shape, dtype=dt, device=on.device)
+            flags |= TTT_FLAG_ZERO_REST
+        rows = _Rows(on, dt)
+        px, po = rows(x, "x", x.shape), rows(out, "out", x.shape)
+        pp, n_pages = _pool(on, pages, n_seq, state_in, state_out)
+        st = (n_pages, width - 1, dim)
+        c = (L * dim, dim)
+        _check(lib().ttt_causal_conv_forward(px, on.need(weight, "weight", torch.float32, (dim, width)),
+                                             on.ptr(bias, "bias", torch.float32, (dim,)), rows.strides(c, c),
+                                             on.ptr(cu_seqlens, "cu_seqlens", torch.int32),
+                                             on.ptr(state_in, "state_in", dt, st), on.ptr(state_out, "state_out", dt, st),
+                                             pp, n_pages, n_seq, L, dim, width, _dtype_code(x), flags, po, on.handle))
         return out
 
 
 def ttt_causal_conv_step(x, state, weight, bias=None, silu: bool = True, pages=None, out=None, stream=None):
     """One token of each sequence through the convolution: x [n_seq, dim]; `state` (a pool [n_pages, width
-    - 1, dim]) moves on by one row in place.  Rows whose page is negative are left out.  Returns out."""
+    - 1, dim]) moves on by one row in place.  Rows whose page is negative give zeros.  Returns out."""
     with _On(x, stream) as on:
         if x.dim() != 2:
             raise ValueError(f"x must be [n_seq, dim], got {tuple(x.shape)}")
         n_seq, dim = x.shape
-        sx = on.rows(x, "x", x.dtype, (n_seq, dim))
-        if weight.dim() != 2:
-            raise ValueError("weight must be [dim, width]")
-        width = weight.shape[1]
-        on.need(weight, "weight", torch.float32, (dim, width))
-        on.maybe(bias, "bias", torch.float32, (dim,))
-        n_pages = _pool(on, pages, n_seq, state)
-        on.need(state, "state", x.dtype, (n_pages, width - 1, dim))
+        width, dt = weight.shape[-1], x.dtype
         if out is None:
-            out = torch.empty((n_seq, dim), dtype=x.dtype, device=on.device) if pages is None else \
-                torch.zeros((n_seq, dim), dtype=x.dtype, device=on.device)
-        so = on.rows(out, "out", x.dtype, (n_seq, dim))
-        _check(lib().ttt_causal_conv_step(_ptr(x), _ptr(weight), _ptr(bias), _strides(sx[1:], so[1:]), _ptr(state),
-                                          _ptr(pages), n_pages, n_seq, dim, width, _dtype_code(x),
-                                          TTT_FLAG_SILU if silu else 0, _ptr(out), on.handle))
+            out = torch.empty((n_seq, dim), dtype=dt, device=on.device)
+        rows = _Rows(on, dt)
+        px, po = rows(x, "x", x.shape), rows(out, "out", x.shape)
+        pp, n_pages = _pool(on, pages, n_seq, state)
+        _check(lib().ttt_causal_conv_step(px, on.need(weight, "weight", torch.float32, (dim, width)),
+                                          on.ptr(bias, "bias", torch.float32, (dim,)), rows.strides((dim,), (dim,)),
+                                          on.need(state, "state", dt, (n_pages, width - 1, dim)), pp, n_pages, n_seq,
+                                          dim, width, _dtype_code(x), TTT_FLAG_SILU if silu else 0, po, on.handle))
         return out
 
 
@@ -760,33 +790,35 @@ def ttt_causal_conv_backward(x, weight, d_out, bias=None, silu: bool = True, sta
                              cu_seqlens=None, workspace=None, stream=None):
     """Gradients of ttt_causal_conv_forward for d_out (and d_state_out, the gradient of the states after
     each sequence; state_in and d_state_out are [n_seq, width - 1, dim] here, sequence b at b).  Returns a
-    dict: dx (x's dtype), dweight [dim, width], dbias [dim] float32 (None without bias), dstate_in (None
-    without state_in)."""
+    dict: dx (x's dtype; zero in rows outside every sequence), dweight [dim, width], dbias [dim] float32
+    (None without bias), dstate_in (None without state_in)."""
     with _On(x, stream) as on:
         n_seq, L, lead = _seq_sizes(x, "x", cu_seqlens)
-        dim = x.shape[-1]
-        sx = on.rows(x, "x", x.dtype, (*lead, dim))
-        sd = on.rows(d_out, "d_out", x.dtype, x.shape)
-        if weight.dim() != 2:
-            raise ValueError("weight must be [dim, width]")
-        width = weight.shape[1]
-        on.need(weight, "weight", torch.float32, (dim, width))
-        on.maybe(bias, "bias", torch.float32, (dim,))
-        on.maybe(cu_seqlens, "cu_seqlens", torch.int32)
-        for n, t in (("state_in", state_in), ("d_state_out", d_state_out)):
-            on.maybe(t, n, x.dtype, (n_seq, width - 1, dim))
-        ws = on.workspace(ttt_causal_conv_backward_workspace_bytes(n_seq, L, dim, width, cu_seqlens is not None, x.dtype),
+        dim, width, dt = x.shape[-1], weight.shape[-1], x.dtype
+        rows = _Rows(on, dt)
+        px, pd = rows(x, "x", x.shape), rows(d_out, "d_out", x.shape)
+        if pd is None:
+            raise TypeError("d_out must be a torch.Tensor")
+        st, c = (n_seq, width - 1, dim), (L * dim, dim)
+        pw = on.need(weight, "weight", torch.float32, (dim, width))
+        ws = on.workspace(ttt_causal_conv_backward_workspace_bytes(n_seq, L, dim, width, cu_seqlens is not None, dt),
                           workspace)
-        g = {"dx": _new_rows(x.shape, x.dtype, on.device, cu_seqlens),
+        g = {"dx": torch.empty(x.shape, dtype=dt, device=on.device),
              "dweight": torch.empty((dim, width), device=on.device),
              "dbias": None if bias is None else torch.empty(dim, device=on.device),
              "dstate_in": None if state_in is None else torch.empty_like(state_in)}
-        _check(lib().ttt_causal_conv_backward(_ptr(x), _ptr(weight), _ptr(bias), _strides(sx, sd), _ptr(cu_seqlens),
-                                              _ptr(state_in), n_seq, L, dim, width, _dtype_code(x),
-                                              TTT_FLAG_SILU if silu else 0, _ptr(d_out), _ptr(d_state_out),
-                                              _ptr(g["dx"]), _ptr(g["dweight"]), _ptr(g["dbias"]), _ptr(g["dstate_in"]),
-                                              _ptr(ws), ws.numel(), on.handle))
+        _check(lib().ttt_causal_conv_backward(px, pw, on.ptr(bias, "bias", torch.float32, (dim,)), rows.strides(c, c),
+                                              on.ptr(cu_seqlens, "cu_seqlens", torch.int32),
+                                              on.ptr(state_in, "state_in", dt, st), n_seq, L, dim, width,
+                                              _dtype_code(x), (TTT_FLAG_SILU if silu else 0) | TTT_FLAG_ZERO_REST, pd,
+                                              on.ptr(d_state_out, "d_state_out", dt, st), g["dx"].data_ptr(),
+                                              g["dweight"].data_ptr(), _addr(g["dbias"]), _addr(g["dstate_in"]),
+                                              ws.data_ptr(), ws.numel(), on.handle))
         return g
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def ttt_selective_scan_ckpt_bytes(n_seq: int, L: int, dim: int, d_state: int, packed: bool = False) -> int:
@@ -806,28 +838,38 @@ def ttt_selective_scan_backward_workspace_bytes(n_seq: int, L: int, dim: int, d_
     return _bytes(lib().ttt_selective_scan_backward_workspace_bytes(n_seq, L, int(packed), dim, groups, d_state))
 
 
-def _scan_operands(on, u, delta, A, B, C, D, z, delta_bias, lead):
-    """Check the scan's inputs (rows of shape `lead`): (dim, groups, d_state, their row strides)."""
-    dim, dt = u.shape[-1], u.dtype
-    if A.dim() != 2:
-        raise ValueError("A must be [dim, d_state]")
-    N = A.shape[1]
-    on.need(A, "A", torch.float32, (dim, N))
+def _scan_operands(on, rows, u, delta, A, B, C, D, z, delta_bias, lead):
+    """Check the scan's inputs (rows of shape `lead`): (dim, groups, d_state), the addresses in the ABI's
+    order, and the strides of contiguous operands."""
+    dim, N = u.shape[-1], A.shape[-1]
     if B.dim() != len(lead) + 2:
         raise ValueError(f"B must be {(*lead, 'groups', 'd_state')}, got {tuple(B.shape)}")
     G = B.shape[-2]
-    s = [on.rows(u, "u", dt, (*lead, dim)), on.rows(delta, "delta", dt, (*lead, dim)),
-         on.rows(B, "B", dt, (*lead, G, N), 2), on.rows(C, "C", dt, (*lead, G, N), 2),
-         (0, 0) if z is None else on.rows(z, "z", dt, (*lead, dim))]
-    on.maybe(D, "D", torch.float32, (dim,))
-    on.maybe(delta_bias, "delta_bias", torch.float32, (dim,))
-    return dim, G, N, s
+    for t, name in ((delta, "delta"), (C, "C")):
+        if t is None:
+            raise TypeError(f"{name} must be a torch.Tensor")
+    wide, narrow = (*lead, dim), (*lead, G, N)
+    pu, pd = rows(u, "u", wide), rows(delta, "delta", wide)
+    pB, pC, pz = rows(B, "B", narrow, 2), rows(C, "C", narrow, 2), rows(z, "z", wide)
+    ptrs = (pu, pd, on.need(A, "A", torch.float32, (dim, N)), pB, pC, on.ptr(D, "D", torch.float32, (dim,)), pz,
+            on.ptr(delta_bias, "delta_bias", torch.float32, (dim,)))
+    if len(lead) == 1:
+        w, n = (dim,), (G * N,)
+    else:
+        w, n = (lead[1] * dim, dim), (lead[1] * G * N, G * N)
+    return dim, G, N, ptrs, (w, w, n, n, w, w)
+
+
+def _packed_strides(contiguous):
+    """Strides of packed rows: the token stride alone stands for (0, token)."""
+    return tuple((0, *c) for c in contiguous)
 
 
 def _check_ckpt(on, ckpt, n_seq, L, dim, N, packed):
-    on.need(ckpt, "ckpt", torch.float32)
+    p = on.need(ckpt, "ckpt", torch.float32)
     if ckpt.numel() * 4 < ttt_selective_scan_ckpt_bytes(n_seq, L, dim, N, packed):
         raise ValueError("ckpt is smaller than ttt_selective_scan_ckpt_bytes(...)")
+    return p
 
 
 def ttt_selective_scan_forward(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus: bool = True,
@@ -838,51 +880,52 @@ def ttt_selective_scan_forward(u, delta, A, B, C, D=None, z=None, delta_bias=Non
     state_in / state_out: float32 pools [n_pages, dim, d_state], in the pages named by `pages` (int32
     [n_seq], default page b).  max_seqlen: the longest packed sequence, if known (it only guides how the
     work is cut up).  ckpt: a float32 tensor of ttt_selective_scan_ckpt_bytes bytes to receive what
-    ttt_selective_scan_backward needs.  Activations may be strided views with contiguous channels.
+    ttt_selective_scan_backward needs.  Activations may be strided views with contiguous channels.  Rows of
+    a given `out` outside every sequence stay as they were; in one allocated here they are zero.
     Returns out (see include/ttt.h)."""
     with _On(u, stream) as on:
         n_seq, L, lead = _seq_sizes(u, "u", cu_seqlens)
-        dim, G, N, s = _scan_operands(on, u, delta, A, B, C, D, z, delta_bias, lead)
         packed = cu_seqlens is not None
-        on.maybe(cu_seqlens, "cu_seqlens", torch.int32)
-        n_pages = _pool(on, pages, n_seq, state_in, state_out)
-        for n, t in (("state_in", state_in), ("state_out", state_out)):
-            on.maybe(t, n, torch.float32, (n_pages, dim, N))
-        if ckpt is not None:
-            _check_ckpt(on, ckpt, n_seq, L, dim, N, packed)
+        flags = TTT_FLAG_SOFTPLUS if softplus else 0
         if out is None:
-            out = _new_rows(u.shape, u.dtype, on.device, cu_seqlens)
-        s.append(on.rows(out, "out", u.dtype, u.shape))
+            out = torch.empty(u.shape, dtype=u.dtype, device=on.device)
+            flags |= TTT_FLAG_ZERO_REST
+        rows = _Rows(on, u.dtype)
+        dim, G, N, ptrs, c = _scan_operands(on, rows, u, delta, A, B, C, D, z, delta_bias, lead)
+        po = rows(out, "out", u.shape)
+        pp, n_pages = _pool(on, pages, n_seq, state_in, state_out)
+        st = (n_pages, dim, N)
+        pc = None if ckpt is None else _check_ckpt(on, ckpt, n_seq, L, dim, N, packed)
         need = ttt_selective_scan_workspace_bytes(n_seq, L, dim, N, G, packed, max_seqlen)
         ws = on.workspace(need, workspace) if need or workspace is not None else None
-        _check(lib().ttt_selective_scan_forward(_ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
-                                                _ptr(delta_bias), _strides(*s), _ptr(cu_seqlens), max_seqlen,
-                                                _ptr(state_in), _ptr(state_out), _ptr(pages), n_pages, n_seq, L, dim,
-                                                G, N, _dtype_code(u), TTT_FLAG_SOFTPLUS if softplus else 0, _ptr(out),
-                                                _ptr(ckpt), _ptr(ws), 0 if ws is None else ws.numel(), on.handle))
+        _check(lib().ttt_selective_scan_forward(*ptrs, rows.strides(*(_packed_strides(c) if packed else c)),
+                                                on.ptr(cu_seqlens, "cu_seqlens", torch.int32), max_seqlen,
+                                                on.ptr(state_in, "state_in", torch.float32, st),
+                                                on.ptr(state_out, "state_out", torch.float32, st), pp, n_pages, n_seq, L,
+                                                dim, G, N, _dtype_code(u), flags, po, pc, _addr(ws),
+                                                0 if ws is None else ws.numel(), on.handle))
         return out
 
 
 def ttt_selective_scan_step(u, delta, A, B, C, state, D=None, z=None, delta_bias=None, softplus: bool = True,
                             pages=None, out=None, stream=None):
     """One token of each sequence through the scan: u, delta, z [n_seq, dim], B, C [n_seq, groups, d_state];
-    `state` (a float32 pool [n_pages, dim, d_state]) is updated in place.  Rows whose page is negative are
-    left out.  Returns out."""
+    `state` (a float32 pool [n_pages, dim, d_state]) is updated in place.  Rows whose page is negative
+    give zeros.  Returns out."""
     with _On(u, stream) as on:
         if u.dim() != 2:
             raise ValueError(f"u must be [n_seq, dim], got {tuple(u.shape)}")
         n_seq = u.shape[0]
-        dim, G, N, s = _scan_operands(on, u, delta, A, B, C, D, z, delta_bias, (n_seq,))
-        n_pages = _pool(on, pages, n_seq, state)
-        on.need(state, "state", torch.float32, (n_pages, dim, N))
         if out is None:
-            out = torch.empty((n_seq, dim), dtype=u.dtype, device=on.device) if pages is None else \
-                torch.zeros((n_seq, dim), dtype=u.dtype, device=on.device)
-        s.append(on.rows(out, "out", u.dtype, u.shape))
-        _check(lib().ttt_selective_scan_step(_ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
-                                             _ptr(delta_bias), _strides(*[p[1:] for p in s]), _ptr(state), _ptr(pages),
-                                             n_pages, n_seq, dim, G, N, _dtype_code(u),
-                                             TTT_FLAG_SOFTPLUS if softplus else 0, _ptr(out), on.handle))
+            out = torch.empty(u.shape, dtype=u.dtype, device=on.device)
+        rows = _Rows(on, u.dtype)
+        dim, G, N, ptrs, c = _scan_operands(on, rows, u, delta, A, B, C, D, z, delta_bias, (n_seq,))
+        po = rows(out, "out", u.shape)
+        pp, n_pages = _pool(on, pages, n_seq, state)
+        _check(lib().ttt_selective_scan_step(*ptrs, rows.strides(*c),
+                                             on.need(state, "state", torch.float32, (n_pages, dim, N)), pp, n_pages, n_seq,
+                                             dim, G, N, _dtype_code(u), TTT_FLAG_SOFTPLUS if softplus else 0, po,
+                                             on.handle))
         return out
 
 
@@ -891,43 +934,49 @@ def ttt_selective_scan_backward(u, delta, A, B, C, d_out, ckpt, D=None, z=None, 
                                 stream=None):
     """Gradients of ttt_selective_scan_forward for d_out (and d_state_out [n_seq, dim, d_state], the gradient
     of the states after each sequence), from the ckpt that the forward wrote.  Returns a dict: du, ddelta,
-    dB, dC, dz (the activations' dtype), dA, dD, ddelta_bias float32, and dstate_in [n_seq, dim, d_state] with
-    state_in_grad; None for inputs that are None."""
+    dB, dC, dz (the activations' dtype; zero in rows outside every sequence), dA, dD, ddelta_bias float32, and
+    dstate_in [n_seq, dim, d_state] with state_in_grad; None for inputs that are None."""
     with _On(u, stream) as on:
         n_seq, L, lead = _seq_sizes(u, "u", cu_seqlens)
-        dim, G, N, s = _scan_operands(on, u, delta, A, B, C, D, z, delta_bias, lead)
-        packed = cu_seqlens is not None
-        on.maybe(cu_seqlens, "cu_seqlens", torch.int32)
-        s.append(on.rows(d_out, "d_out", u.dtype, u.shape))
-        _check_ckpt(on, ckpt, n_seq, L, dim, N, packed)
-        on.maybe(d_state_out, "d_state_out", torch.float32, (n_seq, dim, N))
+        packed, dt, dev = cu_seqlens is not None, u.dtype, on.device
+        rows = _Rows(on, dt)
+        dim, G, N, ptrs, c = _scan_operands(on, rows, u, delta, A, B, C, D, z, delta_bias, lead)
+        pd = rows(d_out, "d_out", u.shape)
+        if pd is None:
+            raise TypeError("d_out must be a torch.Tensor")
+        pc = _check_ckpt(on, ckpt, n_seq, L, dim, N, packed)
+        ps = on.ptr(d_state_out, "d_state_out", torch.float32, (n_seq, dim, N))
         ws = on.workspace(ttt_selective_scan_backward_workspace_bytes(n_seq, L, dim, N, G, packed), workspace)
-        rows = lambda t: _new_rows(t.shape, u.dtype, on.device, cu_seqlens)
-        g = {"du": rows(u), "ddelta": rows(u), "dA": torch.empty((dim, N), device=on.device), "dB": rows(B),
-             "dC": rows(C), "dD": None if D is None else torch.empty(dim, device=on.device),
-             "dz": None if z is None else rows(u),
-             "ddelta_bias": None if delta_bias is None else torch.empty(dim, device=on.device),
-             "dstate_in": torch.empty((n_seq, dim, N), device=on.device) if state_in_grad else None}
-        _check(lib().ttt_selective_scan_backward(_ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
-                                                 _ptr(delta_bias), _strides(*s), _ptr(cu_seqlens), _ptr(ckpt), n_seq, L,
-                                                 dim, G, N, _dtype_code(u), TTT_FLAG_SOFTPLUS if softplus else 0,
-                                                 _ptr(d_out), _ptr(d_state_out), _ptr(g["du"]), _ptr(g["ddelta"]),
-                                                 _ptr(g["dA"]), _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g["dD"]),
-                                                 _ptr(g["dz"]), _ptr(g["ddelta_bias"]), _ptr(g["dstate_in"]), _ptr(ws),
+        new = lambda shape: torch.empty(shape, dtype=dt, device=dev)
+        g = {"du": new(u.shape), "ddelta": new(u.shape), "dA": torch.empty((dim, N), device=dev), "dB": new(B.shape),
+             "dC": new(B.shape), "dD": None if D is None else torch.empty(dim, device=dev),
+             "dz": None if z is None else new(u.shape),
+             "ddelta_bias": None if delta_bias is None else torch.empty(dim, device=dev),
+             "dstate_in": torch.empty((n_seq, dim, N), device=dev) if state_in_grad else None}
+        _check(lib().ttt_selective_scan_backward(*ptrs, rows.strides(*(_packed_strides(c) if packed else c)),
+                                                 on.ptr(cu_seqlens, "cu_seqlens", torch.int32), pc, n_seq, L, dim, G, N,
+                                                 _dtype_code(u), (TTT_FLAG_SOFTPLUS if softplus else 0) | TTT_FLAG_ZERO_REST,
+                                                 pd, ps, g["du"].data_ptr(), g["ddelta"].data_ptr(), g["dA"].data_ptr(),
+                                                 g["dB"].data_ptr(), g["dC"].data_ptr(), _addr(g["dD"]), _addr(g["dz"]),
+                                                 _addr(g["ddelta_bias"]), _addr(g["dstate_in"]), ws.data_ptr(),
                                                  ws.numel(), on.handle))
         return g
 
 
 def _cache_tensors(on, tensors, n_pages):
-    ptrs = (ctypes.c_void_p * max(1, len(tensors)))()
-    sizes = (ctypes.c_longlong * max(1, len(tensors)))()
+    n = len(tensors)
+    ptrs, sizes = (ctypes.c_void_p * max(1, n))(), (ctypes.c_longlong * max(1, n))()
     for k, t in enumerate(tensors):
-        on.need(t, f"tensors[{k}]")
+        ptrs[k] = on.need(t, "a page tensor")
         if t.dim() < 1 or t.shape[0] != n_pages:
             raise ValueError(f"tensors[{k}] must have {n_pages} pages (its first dimension), got {tuple(t.shape)}")
-        ptrs[k] = t.data_ptr()
         sizes[k] = t.numel() // n_pages * t.element_size()
-    return ptrs, sizes, len(tensors)
+    return ptrs, sizes, n, n_pages
+
+
+def _books(on, table, owner):
+    n_rows, n_pages = table.numel(), owner.numel()
+    return on.need(table, "table", torch.int32, (n_rows,)), n_rows, on.need(owner, "owner", torch.int32, (n_pages,)), n_pages
 
 
 def ttt_cache_copy(tensors, src, dst, stream=None):
@@ -937,13 +986,11 @@ def ttt_cache_copy(tensors, src, dst, stream=None):
     with _On(src, stream) as on:
         if not tensors:
             raise ValueError("tensors must name at least one tensor")
-        n, n_pages = src.numel(), tensors[0].shape[0]
-        on.need(src, "src", torch.int32, (n,))
-        on.need(dst, "dst", torch.int32, (n,))
-        t = _cache_tensors(on, tensors, n_pages)
-        copied = torch.empty(n, dtype=torch.int32, device=on.device)
-        ws = torch.empty(1 + 2 * n, dtype=torch.int32, device=on.device)
-        _check(lib().ttt_cache_copy(*t, n_pages, _ptr(src), _ptr(dst), n, _ptr(copied), _ptr(ws), on.handle))
+        n = src.numel()
+        ps, pd = on.need(src, "src", torch.int32, (n,)), on.need(dst, "dst", torch.int32, (n,))
+        t = _cache_tensors(on, tensors, tensors[0].shape[0])
+        copied, ws = torch.empty(3 * n + 1, dtype=torch.int32, device=on.device).split((n, 2 * n + 1))
+        _check(lib().ttt_cache_copy(*t, ps, pd, n, copied.data_ptr(), ws.data_ptr(), on.handle))
         return copied
 
 
@@ -954,28 +1001,21 @@ def ttt_cache_fork(tensors, table, owner, parents, children, stream=None):
     (int32 [n]): the page given to each request, or -1."""
     with _On(table, stream) as on:
         n = children.numel()
-        n_rows, n_pages = table.numel(), owner.numel()
-        on.need(table, "table", torch.int32, (n_rows,))
-        on.need(owner, "owner", torch.int32, (n_pages,))
-        on.need(parents, "parents", torch.int32, (n,))
-        on.need(children, "children", torch.int32, (n,))
+        pt, n_rows, po, n_pages = _books(on, table, owner)
+        pp, pc = on.need(parents, "parents", torch.int32, (n,)), on.need(children, "children", torch.int32, (n,))
         t = _cache_tensors(on, tensors, n_pages)
-        pages = torch.empty(n, dtype=torch.int32, device=on.device)
-        ws = torch.empty(1 + 2 * n, dtype=torch.int32, device=on.device)
-        _check(lib().ttt_cache_fork(*t, n_pages, _ptr(table), n_rows, _ptr(owner), _ptr(parents), _ptr(children), n,
-                                    _ptr(pages), _ptr(ws), on.handle))
+        pages, ws = torch.empty(3 * n + 1, dtype=torch.int32, device=on.device).split((n, 2 * n + 1))
+        _check(lib().ttt_cache_fork(*t, pt, n_rows, po, pp, pc, n, pages.data_ptr(), ws.data_ptr(), on.handle))
         return pages
 
 
 def ttt_cache_free(table, owner, rows, stream=None):
     """Free the pages of the sequence rows (int32 [n]).  Returns the number freed (an int32 tensor)."""
     with _On(table, stream) as on:
-        n, n_rows, n_pages = rows.numel(), table.numel(), owner.numel()
-        on.need(table, "table", torch.int32, (n_rows,))
-        on.need(owner, "owner", torch.int32, (n_pages,))
-        on.need(rows, "rows", torch.int32, (n,))
+        n = rows.numel()
+        books = _books(on, table, owner)
         freed = torch.empty((), dtype=torch.int32, device=on.device)
-        _check(lib().ttt_cache_free(_ptr(table), n_rows, _ptr(owner), n_pages, _ptr(rows), n, _ptr(freed), on.handle))
+        _check(lib().ttt_cache_free(*books, on.need(rows, "rows", torch.int32, (n,)), n, freed.data_ptr(), on.handle))
         return freed
 
 
@@ -984,13 +1024,8 @@ def ttt_cache_compact(tensors, table, owner, stream=None):
     steps.  Returns (live, new_page): the number of live pages (an int32 tensor) and the new page of each
     old one (int32 [n_pages], -1 where it was free)."""
     with _On(table, stream) as on:
-        n_rows, n_pages = table.numel(), owner.numel()
-        on.need(table, "table", torch.int32, (n_rows,))
-        on.need(owner, "owner", torch.int32, (n_pages,))
+        pt, n_rows, po, n_pages = _books(on, table, owner)
         t = _cache_tensors(on, tensors, n_pages)
-        live = torch.empty((), dtype=torch.int32, device=on.device)
-        new_page = torch.empty(n_pages, dtype=torch.int32, device=on.device)
-        ws = torch.empty(2 + n_pages, dtype=torch.int32, device=on.device)
-        _check(lib().ttt_cache_compact(*t, n_pages, _ptr(table), n_rows, _ptr(owner), _ptr(live), _ptr(new_page),
-                                       _ptr(ws), on.handle))
-        return live, new_page
+        live, new_page, ws = torch.empty(2 * n_pages + 3, dtype=torch.int32, device=on.device).split((1, n_pages, n_pages + 2))
+        _check(lib().ttt_cache_compact(*t, pt, n_rows, po, live.data_ptr(), new_page.data_ptr(), ws.data_ptr(), on.handle))
+        return live[0], new_page

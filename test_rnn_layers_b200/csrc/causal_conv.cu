@@ -18,10 +18,14 @@ constexpr int kThreads = 128;
 
 template <typename T, int W, int VEC>
 __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvArgs a) {
-    Piece p;
-    if (!find_piece(a.s, blockIdx.x, a.span, p)) return;
     const int d = (blockIdx.y * kThreads + threadIdx.x) * VEC;
     if (d >= a.D) return;
+    each_rest_row(a.s, blockIdx.x, gridDim.x, [&](long long r) {
+        const float zero[VEC] = {};
+        store_vec<VEC>(static_cast<T*>(a.out) + r * a.so.t + d, zero);
+    });
+    Piece p;
+    if (!find_piece(a.s, blockIdx.x, a.span, p)) return;
     const T* x = static_cast<const T*>(a.x) + p.row * a.sx.b + p.t0 * a.sx.t + d;
     T* out = static_cast<T*>(a.out) + p.row * a.so.b + p.t0 * a.so.t + d;
     const int page = page_of(a.pages, a.n_pages, p.b);
@@ -103,7 +107,11 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvArgs a) {
     const int b = static_cast<int>(i / per), d = static_cast<int>(i % per) * VEC;
     if (b >= a.s.n_seq) return;
     const int page = page_of(a.pages, a.n_pages, b);
-    if (page < 0) return;
+    if (page < 0) {
+        const float zero[VEC] = {};
+        store_vec<VEC>(static_cast<T*>(a.out) + b * a.so.b + d, zero);
+        return;
+    }
     T* state = static_cast<T*>(a.state_out) + (static_cast<long long>(page) * (W - 1)) * a.D + d;
     float win[W][VEC], y[VEC];
 #pragma unroll
@@ -132,6 +140,10 @@ template <typename T, int W, int VEC>
 __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvBwdArgs a) {
     const int d = (blockIdx.y * kThreads + threadIdx.x) * VEC;
     if (d >= a.D) return;
+    each_rest_row(a.s, blockIdx.x, gridDim.x, [&](long long r) {
+        const float zero[VEC] = {};
+        store_vec<VEC>(static_cast<T*>(a.dx) + r * a.D + d, zero);
+    });
     float* part = a.part + static_cast<long long>(blockIdx.x) * (W + 1) * a.D + d;
     float gw[W][VEC], gb[VEC];
 #pragma unroll

@@ -28,189 +28,359 @@
 namespace ttt {
 namespace {
 
-constexpr int kWarps = 8;
 constexpr int kTile = 16;
 
-enum Mode { kWhole, kSpanState, kSpanOut };
+enum Mode { kSpanState, kOut, kOutGated };
 
-// Four states of a lane, n .. n + 3 of `N`; PAD: N is not 4 P, so the last lanes hold fewer.
-template <bool PAD>
-__device__ __forceinline__ void load_state(const float* p, int left, float (&h)[4]) {
-    if constexpr (!PAD) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        h[0] = v.x; h[1] = v.y; h[2] = v.z; h[3] = v.w;
+// The S states of a lane, of which the last lanes may hold fewer (`left`) when PAD.
+template <int S, bool PAD>
+__device__ __forceinline__ void load_state(const float* p, int left, float (&h)[S]) {
+    if constexpr (PAD) {
+#pragma unroll
+        for (int i = 0; i < S; ++i) h[i] = i < left ? p[i] : 0.f;
+    } else if constexpr (S == 2) {
+        load_vec<2>(p, h);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = i < left ? p[i] : 0.f;
+        for (int i = 0; i < S; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(p + i);
+            h[i] = v.x; h[i + 1] = v.y; h[i + 2] = v.z; h[i + 3] = v.w;
+        }
     }
 }
-template <bool PAD>
-__device__ __forceinline__ void store_state(float* p, int left, const float (&h)[4]) {
-    if constexpr (!PAD) {
-        *reinterpret_cast<float4*>(p) = make_float4(h[0], h[1], h[2], h[3]);
-    } else {
+template <int S, bool PAD>
+__device__ __forceinline__ void store_state(float* p, int left, const float (&h)[S]) {
+    if constexpr (PAD) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < S; ++i)
             if (i < left) p[i] = h[i];
+    } else if constexpr (S == 2) {
+        store_vec<2>(p, h);
+    } else {
+#pragma unroll
+        for (int i = 0; i < S; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
+    }
+}
+template <int S, bool PAD>
+__device__ __forceinline__ void load_state(const float* p, int left, f32x2 (&h)[S / 2]) {
+    float v[S];
+    load_state<S, PAD>(p, left, v);
+#pragma unroll
+    for (int i = 0; i < S / 2; ++i) h[i] = pack2(v[2 * i], v[2 * i + 1]);
+}
+template <int S, bool PAD>
+__device__ __forceinline__ void store_state(float* p, int left, const f32x2 (&h)[S / 2]) {
+    float v[S];
+#pragma unroll
+    for (int i = 0; i < S / 2; ++i) unpack2(h[i], v[2 * i], v[2 * i + 1]);
+    store_state<S, PAD>(p, left, v);
+}
+
+// S floats of shared memory as pairs.
+template <int S>
+__device__ __forceinline__ void load_pairs(const float* p, f32x2 (&v)[S / 2]) {
+    if constexpr (S == 2) {
+        v[0] = *reinterpret_cast<const f32x2*>(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < S / 2; i += 2) {
+            const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(p + 2 * i);
+            v[i] = t.x; v[i + 1] = t.y;
+        }
     }
 }
 
-template <typename T, int P, bool PAD, int MODE>
-__global__ void __launch_bounds__(kWarps * 32) scan_kernel(const ScanArgs a) {
-    constexpr int CPW = 32 / P, CH = kWarps * CPW, NP = 4 * P;
+__device__ __forceinline__ void cp_async_16(void* smem, const void* gmem) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Layout of the lanes: P lanes a channel with S states each, R channels a lane, NW warps a block.
+template <int S_, int P_, int R_, int NW_>
+struct Lanes {
+    static constexpr int S = S_, P = P_, R = R_, NW = NW_, CPW = 32 / P, CH = NW * CPW * R, NP = S * P, THREADS = NW * 32;
+};
+
+// The layouts, by the number of states N.  Four states a lane and one channel a lane for N = 16: two
+// channels a lane read B and C half as often but leave 1.7 warps for each scheduler at the sizes of a
+// training batch, eight states a lane likewise (8 x 2048 tokens, 2048 channels: 353 us against 389 and
+// 386 us; two states a lane 500 us; four warps a block instead of eight 382 us).
+using Lanes4 = Lanes<4, 1, 1, 2>;
+using Lanes8 = Lanes<4, 2, 1, 4>;
+using Lanes16 = Lanes<4, 4, 1, 8>;
+using Lanes32 = Lanes<4, 8, 2, 8>;
+using Lanes64 = Lanes<8, 8, 1, 8>;
+
+template <typename T, class Y, bool PAD, int MODE>
+__global__ void __launch_bounds__(Y::THREADS) scan_kernel(const ScanArgs a) {
+    constexpr int S = Y::S, P = Y::P, R = Y::R, NW = Y::NW, CPW = Y::CPW, CH = Y::CH, NP = Y::NP, TH = Y::THREADS;
     constexpr int K = kTile / P;                     // tokens of a tile that a lane finishes
     constexpr int BC = kTile * 2 * NP;               // values of B and C of a tile
-    constexpr int NB = (BC + kWarps * 32 - 1) / (kWarps * 32);
-    __shared__ __align__(16) float sbc[2][BC];       // [token][B, C][n]
-    __shared__ float2 sdt[kWarps][kTile][CPW];       // (dt, dt u)
+    constexpr int NB = (BC + TH - 1) / TH;
+    constexpr int VE = 16 / sizeof(T);               // channels of a 16-byte piece
+    constexpr int PIECES = kTile * CH / VE;          // pieces of a tile of one operand
+    constexpr bool OUT = MODE != kSpanState, GATE = MODE == kOutGated;
+    // A row is padded by one warp's channels: the P rows that a warp reads at once lie in other banks.
+    constexpr int ROW = CH + (CPW * sizeof(T) >= 16 ? CPW : VE);
+    __shared__ __align__(16) T raw[2][GATE ? 3 : 2][kTile][ROW];  // u (later out), delta, z
+    __shared__ __align__(16) float sbc[2][BC];                    // [token][B, C][n]
+    __shared__ __align__(16) float2 sdt[NW][kTile][R * CPW];             // (dt, dt u)
 
     const int r = a.dim / a.groups, tiles = (r + CH - 1) / CH;
-    const int ct = blockIdx.x % (a.groups * tiles), g = ct / tiles;
+    const int ct = blockIdx.x % (a.groups * tiles), g = ct / tiles, c0 = (ct % tiles) * CH;
+    if (OUT)
+        each_rest_row(a.s, blockIdx.x / (a.groups * tiles), a.n_slots, [&](long long row) {
+            for (int k = threadIdx.x; k < CH; k += TH)
+                if (c0 + k < r) static_cast<T*>(a.out)[row * a.so.t + g * r + c0 + k] = from_f32<T>(0.f);
+        });
     Piece p;
-    int first, last;
     if (!find_piece(a.s, blockIdx.x / (a.groups * tiles), a.span, p)) return;
-    first = p.tile * a.span;
-    last = min(first + a.span, p.len);
+    const int first = p.tile * a.span, last = min(first + a.span, p.len);
     if (MODE == kSpanState && p.tile > 0 && last == p.len) return;  // nothing starts from the last span
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane / CPW, c = lane % CPW;
-    const int cg = (ct % tiles) * CH + warp * CPW + c;   // channel within the group
-    const bool live = cg < r;
-    const int d = g * r + (live ? cg : r - 1);
-    const int left = a.N - 4 * q;
-    const long long hoff = static_cast<long long>(d) * a.N + 4 * q, hrow = static_cast<long long>(a.dim) * a.N;
-
-    float A2[4], h[4] = {0.f, 0.f, 0.f, 0.f};
-    load_state<PAD>(a.A + hoff, left, A2);
+    const int cb = warp * CPW * R + c;               // the lane's first channel within the block; the others CPW apart
+    const int left = a.N - S * q;
+    const long long hrow = static_cast<long long>(a.dim) * a.N;
+    bool live[R];
+    int d[R];
+    long long hoff[R];
+    f32x2 A2[R][S / 2], h[R][S / 2];
+    float bias[R], Dk[R];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) A2[i] *= kLog2e;
-    const float bias = a.bias ? a.bias[d] : 0.f, Dk = a.D ? a.D[d] : 0.f;
+    for (int m = 0; m < R; ++m) {
+        live[m] = c0 + cb + m * CPW < r;
+        d[m] = g * r + (live[m] ? c0 + cb + m * CPW : r - 1);
+        hoff[m] = static_cast<long long>(d[m]) * a.N + S * q;
+        load_state<S, PAD>(a.A + hoff[m], left, A2[m]);
+#pragma unroll
+        for (int i = 0; i < S / 2; ++i) {
+            A2[m][i] = mul2(A2[m][i], both(kLog2e));
+            h[m][i] = both(0.f);
+        }
+        bias[m] = a.bias ? a.bias[d[m]] : 0.f;
+        Dk[m] = a.D ? a.D[d[m]] : 0.f;
+    }
 
     const int page = page_of(a.pages, a.n_pages, p.b);
-    if (MODE == kWhole || (MODE == kSpanState && p.tile == 0)) {
-        if (a.state_in && page >= 0) load_state<PAD>(a.state_in + page * hrow + hoff, left, h);
-        if (MODE == kSpanState && live) store_state<PAD>(a.seg_h0 + p.b * hrow + hoff, left, h);
-        if (MODE == kSpanState && last == p.len) return;
-    } else if (MODE == kSpanOut) {
-        if (p.tile == 0) {
-            load_state<PAD>(a.seg_h0 + p.b * hrow + hoff, left, h);
-        } else {
-            const int s0 = p.slot - p.tile;
-            load_state<PAD>(a.seg_h + s0 * hrow + hoff, left, h);
-            for (int s = s0 + 1; s < p.slot; ++s) {
-                float e[4];
-                load_state<PAD>(a.seg_h + s * hrow + hoff, left, e);
-                const float sum = a.seg_dt[static_cast<long long>(s) * a.dim + d];
+    if (OUT ? !a.split : p.tile == 0) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) h[i] = fmaf(decay2(sum * A2[i]), h[i], e[i]);
+        for (int m = 0; m < R; ++m) {
+            if (a.state_in && page >= 0) load_state<S, PAD>(a.state_in + page * hrow + hoff[m], left, h[m]);
+            if (MODE == kSpanState && live[m]) store_state<S, PAD>(a.seg_h0 + p.b * hrow + hoff[m], left, h[m]);
+        }
+        if (MODE == kSpanState && last == p.len) return;
+    } else if (OUT) {
+#pragma unroll
+        for (int m = 0; m < R; ++m) {
+            if (p.tile == 0) {
+                load_state<S, PAD>(a.seg_h0 + p.b * hrow + hoff[m], left, h[m]);
+            } else {
+                const int s0 = p.slot - p.tile;
+                load_state<S, PAD>(a.seg_h + s0 * hrow + hoff[m], left, h[m]);
+                for (int s = s0 + 1; s < p.slot; ++s) {
+                    f32x2 e[S / 2];
+                    load_state<S, PAD>(a.seg_h + s * hrow + hoff[m], left, e);
+                    const float sum = a.seg_dt[static_cast<long long>(s) * a.dim + d[m]];
+#pragma unroll
+                    for (int i = 0; i < S / 2; ++i) h[m][i] = fma2(decay2(mul2(both(sum), A2[m][i])), h[m][i], e[i]);
+                }
             }
         }
     }
 
-    const T* u = static_cast<const T*>(a.u) + p.row * a.su.b + p.t0 * a.su.t + d;
-    const T* dl = static_cast<const T*>(a.delta) + p.row * a.sdt.b + p.t0 * a.sdt.t + d;
-    const T* z = a.z ? static_cast<const T*>(a.z) + p.row * a.sz.b + p.t0 * a.sz.t + d : nullptr;
+    // the block's channels of this sequence's rows
+    const long long at0 = g * r + c0;
+    const T* u = static_cast<const T*>(a.u) + p.row * a.su.b + p.t0 * a.su.t + at0;
+    const T* dl = static_cast<const T*>(a.delta) + p.row * a.sdt.b + p.t0 * a.sdt.t + at0;
+    const T* z = static_cast<const T*>(a.z) + p.row * a.sz.b + p.t0 * a.sz.t + at0;
     const T* Bm = static_cast<const T*>(a.B) + p.row * a.sB.b + p.t0 * a.sB.t + g * a.N;
     const T* Cm = static_cast<const T*>(a.C) + p.row * a.sC.b + p.t0 * a.sC.t + g * a.N;
-    T* out = static_cast<T*>(a.out) + p.row * a.so.b + p.t0 * a.so.t + d;
+    T* out = static_cast<T*>(a.out) + p.row * a.so.b + p.t0 * a.so.t + at0;
     long long chunk = 0;
-    if (MODE != kSpanState && a.ckpt)
+    if (OUT && a.ckpt)
         chunk = a.s.cu ? slot_base(a.s.cu, p.b, a.s.L, kScanChunk)
                        : p.b * ((a.s.L + kScanChunk - 1) / kScanChunk);
 
-    T ru[K], rd[K], rz[K], rbc[NB];
-    auto load_tile = [&](int t0) {
+    // One 16-byte piece of a tile's row: asynchronously where it lies on a 16-byte boundary.
+    auto fetch = [&](T* to, const T* from, bool wide, int ch) {
+        if (wide) {
+            cp_async_16(to, from);
+        } else {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int t = t0 + k * P + q;
-            ru[k] = rd[k] = rz[k] = from_f32<T>(0.f);
-            if (t < last) {
-                ru[k] = u[t * a.su.t];
-                rd[k] = dl[t * a.sdt.t];
-                if (MODE != kSpanState && z) rz[k] = z[t * a.sz.t];
+            for (int i = 0; i < VE; ++i)
+                if (c0 + ch + i < r) to[i] = from[i];
+        }
+    };
+    auto store_out = [&](int buf, int t0) {          // the tile's outputs, left where u was
+        for (int e = threadIdx.x; e < PIECES; e += TH) {
+            const int t = e / (CH / VE), ch = e % (CH / VE) * VE;
+            if (t0 + t < last) {
+                const T* from = &raw[buf][0][t][ch];
+                T* to = out + (t0 + t) * a.so.t + ch;
+                if (a.wide & 8 && c0 + ch + VE <= r) {
+                    *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VE; ++i)
+                        if (c0 + ch + i < r) to[i] = from[i];
+                }
             }
         }
+    };
+    auto load_raw = [&](int buf, int t0) {
+        for (int e = threadIdx.x; e < PIECES; e += TH) {
+            const int t = e / (CH / VE), ch = e % (CH / VE) * VE;
+            if (t0 + t < last) {
+                const bool in = c0 + ch + VE <= r;
+                fetch(&raw[buf][0][t][ch], u + (t0 + t) * a.su.t + ch, in && (a.wide & 1), ch);
+                fetch(&raw[buf][1][t][ch], dl + (t0 + t) * a.sdt.t + ch, in && (a.wide & 2), ch);
+                if (GATE) fetch(&raw[buf][GATE ? 2 : 0][t][ch], z + (t0 + t) * a.sz.t + ch, in && (a.wide & 4), ch);
+            }
+        }
+    };
+    T rbc[NB];
+    auto load_bc = [&](int t0) {
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            const int e = k * kWarps * 32 + threadIdx.x, t = t0 + e / (2 * NP), n = e % NP;
+            const int e = k * TH + threadIdx.x, t = t0 + e / (2 * NP), n = e % NP;
             rbc[k] = from_f32<T>(0.f);
             if (e < BC && t < last && (!PAD || n < a.N))
                 rbc[k] = (e / NP) & 1 ? Cm[t * a.sC.t + n] : Bm[t * a.sB.t + n];
         }
     };
 
-    float sum_dt = 0.f;
+    float sum_dt[R] = {};
     int buf = 0;
-    load_tile(first);
+    if (first < last) {
+        load_raw(0, first);
+        load_bc(first);
+    }
     for (int t0 = first; t0 < last; t0 += kTile, buf ^= 1) {
-        float fu[K], fz[K];
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            const int e = k * kWarps * 32 + threadIdx.x;
+            const int e = k * TH + threadIdx.x;
             if (e < BC) sbc[buf][e] = to_f32(rbc[k]);
         }
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            fu[k] = to_f32(ru[k]);
-            fz[k] = to_f32(rz[k]);
-            float dt = to_f32(rd[k]) + bias;
-            if (a.softplus) dt = softplus_f(dt);
-            if (t0 + k * P + q >= last) dt = 0.f;
-            sum_dt += dt;
-            sdt[warp][k * P + q][c] = make_float2(dt, dt * fu[k]);
+        cp_async_wait();
+        __syncthreads();  // this tile is there, and the one before is done with
+        if (OUT && t0 > first) store_out(buf ^ 1, t0 - kTile);
+        if (t0 + kTile < last) {
+            load_raw(buf ^ 1, t0 + kTile);  // each thread refills the pieces that it has just stored
+            load_bc(t0 + kTile);
         }
-        __syncthreads();  // B and C of this tile; the other buffer is read no more
-        if (t0 + kTile < last) load_tile(t0 + kTile);
-
-        auto tokens = [&](auto full) {
-            constexpr bool FULL = decltype(full)::value;
-            const int n = FULL ? kTile : last - t0;
+        float fu[R][K], fz[R][K];
+#pragma unroll
+        for (int m = 0; m < R; ++m)
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                float y[P];
+                const int t = k * P + q, ch = cb + m * CPW;
+                fu[m][k] = to_f32(raw[buf][0][t][ch]);
+                fz[m][k] = GATE ? silu_f(to_f32(raw[buf][GATE ? 2 : 0][t][ch])) : 1.f;
+                float dt = to_f32(raw[buf][1][t][ch]) + bias[m];
+                if (a.softplus) dt = softplus_f(dt);
+                if (MODE == kSpanState && t0 + t < last) sum_dt[m] += dt;
+                sdt[warp][t][m * CPW + c] = make_float2(dt, dt * fu[m][k]);
+            }
+        __syncwarp();
+
+        // Tokens t1 .. t1 + 7 of the tile, in groups of up to P whose sums over the lanes are taken
+        // together.  Straight-line code: the decay factors do not wait for the states, so the
+        // compiler can run ahead with them.
+        auto tokens = [&](auto full, int t1) {
+            constexpr bool FULL = decltype(full)::value;
+            constexpr int G = P < kScanChunk ? P : kScanChunk;
+            const int n = FULL ? kTile : last - t0;
+            float y[R][kScanChunk];
+            // the factors of all eight tokens first: their loads, exponentials and polynomials overlap
+            f32x2 f[R][kScanChunk][S / 2], du[R][kScanChunk];
 #pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    const int t = k * P + j;
-                    y[j] = 0.f;
-                    if (FULL || t < n) {
-                        if (MODE != kSpanState && a.ckpt && t % kScanChunk == 0 && live)
-                            store_state<PAD>(a.ckpt + (chunk + (t0 + t) / kScanChunk) * hrow + hoff, left, h);
-                        const float2 v = sdt[warp][t][c];
-                        const float4 b4 = *reinterpret_cast<const float4*>(&sbc[buf][(2 * t) * NP + 4 * q]);
-                        const float b[4] = {b4.x, b4.y, b4.z, b4.w};
+            for (int j = 0; j < kScanChunk; ++j)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            h[i] = fmaf(decay2(v.x * A2[i]), h[i], v.y * b[i]);
-                            if (PAD && i >= left) h[i] = 0.f;
+                for (int m = 0; m < R; ++m) {
+                    const float2 v = sdt[warp][t1 + j][m * CPW + c];
+                    const f32x2 dt = both(v.x);
+                    du[m][j] = both(v.y);
+#pragma unroll
+                    for (int i = 0; i < S / 2; ++i) f[m][j][i] = decay2(mul2(dt, A2[m][i]));
+                }
+#pragma unroll
+            for (int j = 0; j < kScanChunk; ++j) {
+                const int t = t1 + j;
+#pragma unroll
+                for (int m = 0; m < R; ++m) y[m][j] = 0.f;
+                if (FULL || t < n) {
+                    f32x2 b[S / 2], cc[S / 2];
+                    load_pairs<S>(&sbc[buf][(2 * t) * NP + S * q], b);
+                    if (OUT) load_pairs<S>(&sbc[buf][(2 * t + 1) * NP + S * q], cc);
+#pragma unroll
+                    for (int m = 0; m < R; ++m) {
+                        f32x2 acc = 0;
+#pragma unroll
+                        for (int i = 0; i < S / 2; ++i) {
+                            h[m][i] = fma2(f[m][j][i], h[m][i], mul2(du[m][j], b[i]));
+                            if (PAD) {
+                                float lo, hi;
+                                unpack2(h[m][i], lo, hi);
+                                h[m][i] = pack2(2 * i < left ? lo : 0.f, 2 * i + 1 < left ? hi : 0.f);
+                            }
+                            if (OUT) acc = i ? fma2(cc[i], h[m][i], acc) : mul2(cc[i], h[m][i]);
                         }
-                        if (MODE != kSpanState) {
-                            const float4 c4 = *reinterpret_cast<const float4*>(&sbc[buf][(2 * t + 1) * NP + 4 * q]);
-                            y[j] = fmaf(c4.x, h[0], c4.y * h[1]) + fmaf(c4.z, h[2], c4.w * h[3]);
+                        if (OUT) {
+                            float lo, hi;
+                            unpack2(acc, lo, hi);
+                            y[m][j] = lo + hi;
                         }
                     }
                 }
-                if (MODE != kSpanState) {
-                    float v = reduce_across<P, CPW>(y, q);
-                    const int t = t0 + k * P + q;
-                    v = fmaf(Dk, fu[k], v);
-                    if (z) v *= silu_f(fz[k]);
-                    if (live && (FULL || t < last)) out[t * a.so.t] = from_f32<T>(v);
-                }
+            }
+            if (OUT) {
+#pragma unroll
+                for (int m = 0; m < R; ++m)
+#pragma unroll
+                    for (int j = 0; j < kScanChunk; j += G) {
+                        float w[G];
+#pragma unroll
+                        for (int i = 0; i < G; ++i) w[i] = y[m][j + i];
+                        float v = reduce_across<G, CPW>(w, q);
+                        if (P > G) v += __shfl_xor_sync(0xffffffffu, v, G * CPW);
+                        const int k = (t1 + j) / P;
+                        raw[buf][0][k * P + q][cb + m * CPW] = from_f32<T>(fmaf(Dk[m], fu[m][k], v) * fz[m][k]);
+                    }
             }
         };
-        if (t0 + kTile <= last) tokens(std::true_type{});
-        else tokens(std::false_type{});
-        __syncwarp();  // sdt is read no more
-    }
-    if (MODE == kSpanState) {
+        const bool full = t0 + kTile <= last;
+        if (OUT && a.ckpt) {
 #pragma unroll
-        for (int w = P / 2; w >= 1; w /= 2) sum_dt += __shfl_xor_sync(0xffffffffu, sum_dt, w * CPW);
-        if (live) {
-            store_state<PAD>(a.seg_h + p.slot * hrow + hoff, left, h);
-            if (q == 0) a.seg_dt[static_cast<long long>(p.slot) * a.dim + d] = sum_dt;
+            for (int m = 0; m < R; ++m)
+                if (live[m]) store_state<S, PAD>(a.ckpt + (chunk + t0 / kScanChunk) * hrow + hoff[m], left, h[m]);
         }
-    } else if (a.state_out && page >= 0 && live && last == p.len) {
-        store_state<PAD>(a.state_out + page * hrow + hoff, left, h);
+        if (full) tokens(std::true_type{}, 0);
+        else tokens(std::false_type{}, 0);
+        if (OUT && a.ckpt && t0 + kScanChunk < last) {
+#pragma unroll
+            for (int m = 0; m < R; ++m)
+                if (live[m]) store_state<S, PAD>(a.ckpt + (chunk + t0 / kScanChunk + 1) * hrow + hoff[m], left, h[m]);
+        }
+        if (full) tokens(std::true_type{}, kScanChunk);
+        else tokens(std::false_type{}, kScanChunk);
+    }
+    if (OUT && first < last) {
+        __syncthreads();
+        store_out(buf ^ 1, first + (last - first - 1) / kTile * kTile);
+    }
+#pragma unroll
+    for (int m = 0; m < R; ++m) {
+        if (MODE == kSpanState) {
+#pragma unroll
+            for (int w = P / 2; w >= 1; w /= 2) sum_dt[m] += __shfl_xor_sync(0xffffffffu, sum_dt[m], w * CPW);
+            if (live[m]) {
+                store_state<S, PAD>(a.seg_h + p.slot * hrow + hoff[m], left, h[m]);
+                if (q == 0) a.seg_dt[static_cast<long long>(p.slot) * a.dim + d[m]] = sum_dt[m];
+            }
+        } else if (a.state_out && page >= 0 && live[m] && last == p.len) {
+            store_state<S, PAD>(a.state_out + page * hrow + hoff[m], left, h[m]);
+        }
     }
 }
 
@@ -227,8 +397,8 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanStepArgs a) {
         const int left = a.N - 4 * q, g = d / (a.dim / a.groups), n = g * a.N + 4 * q;
         float* hp = a.state + (static_cast<long long>(page) * a.dim + d) * a.N + 4 * q;
         float h[4], A[4];
-        load_state<PAD>(hp, left, h);
-        load_state<PAD>(a.A + static_cast<long long>(d) * a.N + 4 * q, left, A);
+        load_state<4, PAD>(hp, left, h);
+        load_state<4, PAD>(a.A + static_cast<long long>(d) * a.N + 4 * q, left, A);
         u = to_f32(static_cast<const T*>(a.u)[b * a.su + d]);
         float dt = to_f32(static_cast<const T*>(a.delta)[b * a.sdt + d]) + (a.bias ? a.bias[d] : 0.f);
         if (a.softplus) dt = softplus_f(dt);
@@ -241,30 +411,30 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanStepArgs a) {
                 y = fmaf(to_f32(Cm[i]), h[i], y);
             }
         }
-        store_state<PAD>(hp, left, h);
+        store_state<4, PAD>(hp, left, h);
     }
 #pragma unroll
     for (int w = P / 2; w >= 1; w /= 2) y += __shfl_xor_sync(0xffffffffu, y, w);
-    if (on && q == 0) {
-        y = fmaf(a.D ? a.D[d] : 0.f, u, y);
-        if (a.z) y *= silu_f(to_f32(static_cast<const T*>(a.z)[b * a.sz + d]));
+    if (b < a.n_seq && q == 0) {
+        if (on) {
+            y = fmaf(a.D ? a.D[d] : 0.f, u, y);
+            if (a.z) y *= silu_f(to_f32(static_cast<const T*>(a.z)[b * a.sz + d]));
+        }
         static_cast<T*>(a.out)[b * a.so + d] = from_f32<T>(y);
     }
 }
 
-template <typename T, int P, bool PAD>
+template <typename T, class Y, bool PAD>
 cudaError_t run(const ScanArgs& a, cudaStream_t s) {
-    constexpr int CH = kWarps * 32 / P;
-    const int r = a.dim / a.groups, tiles = a.groups * ((r + CH - 1) / CH);
+    const int r = a.dim / a.groups, tiles = a.groups * ((r + Y::CH - 1) / Y::CH);
     const unsigned grid = static_cast<unsigned>(static_cast<long long>(a.n_slots) * tiles);
-    if (!a.split) {
-        scan_kernel<T, P, PAD, kWhole><<<grid, kWarps * 32, 0, s>>>(a);
-    } else {
-        scan_kernel<T, P, PAD, kSpanState><<<grid, kWarps * 32, 0, s>>>(a);
+    if (a.split) {
+        scan_kernel<T, Y, PAD, kSpanState><<<grid, Y::THREADS, 0, s>>>(a);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        scan_kernel<T, P, PAD, kSpanOut><<<grid, kWarps * 32, 0, s>>>(a);
     }
+    if (a.z) scan_kernel<T, Y, PAD, kOutGated><<<grid, Y::THREADS, 0, s>>>(a);
+    else scan_kernel<T, Y, PAD, kOut><<<grid, Y::THREADS, 0, s>>>(a);
     return cudaGetLastError();
 }
 template <typename T, int P, bool PAD>
@@ -274,35 +444,53 @@ cudaError_t run_step(const ScanStepArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// Lanes a channel: the fewest that hold N states, 4 each.
-template <typename T, class Args, class F>
-cudaError_t by_states(const Args& a, F f) {
-    if (a.N <= 4) return f(std::integral_constant<int, 1>{});
-    if (a.N <= 8) return f(std::integral_constant<int, 2>{});
-    if (a.N <= 16) return f(std::integral_constant<int, 4>{});
-    if (a.N <= 32) return f(std::integral_constant<int, 8>{});
-    return f(std::integral_constant<int, 16>{});
+template <typename T, class Y>
+cudaError_t pad(const ScanArgs& a, cudaStream_t s) {
+    return a.N == Y::NP ? run<T, Y, false>(a, s) : run<T, Y, true>(a, s);
 }
+template <typename T, int P>
+cudaError_t pad_step(const ScanStepArgs& a, cudaStream_t s) {
+    return a.N == 4 * P ? run_step<T, P, false>(a, s) : run_step<T, P, true>(a, s);
+}
+
+// The fewest lanes a channel that hold N states.
 template <typename T>
 cudaError_t dispatch(const ScanArgs& a, cudaStream_t s) {
-    return by_states<T>(a, [&](auto p) {
-        constexpr int P = decltype(p)::value;
-        return a.N == 4 * P ? run<T, P, false>(a, s) : run<T, P, true>(a, s);
-    });
+    if (a.N <= 4) return pad<T, Lanes4>(a, s);
+    if (a.N <= 8) return pad<T, Lanes8>(a, s);
+    if (a.N <= 16) return pad<T, Lanes16>(a, s);
+    if (a.N <= 32) return pad<T, Lanes32>(a, s);
+    return pad<T, Lanes64>(a, s);
 }
 template <typename T>
 cudaError_t dispatch_step(const ScanStepArgs& a, cudaStream_t s) {
-    return by_states<T>(a, [&](auto p) {
-        constexpr int P = decltype(p)::value;
-        return a.N == 4 * P ? run_step<T, P, false>(a, s) : run_step<T, P, true>(a, s);
-    });
+    if (a.N <= 4) return pad_step<T, 1>(a, s);
+    if (a.N <= 8) return pad_step<T, 2>(a, s);
+    if (a.N <= 16) return pad_step<T, 4>(a, s);
+    if (a.N <= 32) return pad_step<T, 8>(a, s);
+    return pad_step<T, 16>(a, s);
+}
+
+int lanes_channels(int N) {
+    return N <= 4 ? Lanes4::CH : N <= 8 ? Lanes8::CH : N <= 16 ? Lanes16::CH :
+           N <= 32 ? Lanes32::CH : Lanes64::CH;
+}
+
+// Whether the rows of the block's channels start on 16-byte boundaries.
+bool rows_on_16(const void* p, RowStride r, const ScanArgs& a, size_t esz) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (a.s.cu || r.b * esz % 16 == 0) && r.t * esz % 16 == 0 &&
+           (a.groups == 1 || a.dim / a.groups * esz % 16 == 0);
 }
 
 }  // namespace
 
-int scan_channels(int N) { return kWarps * 32 / (N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16); }
+int scan_channels(int N) { return lanes_channels(N); }
 
-cudaError_t launch_scan(const ScanArgs& a, int dtype, cudaStream_t s) {
+cudaError_t launch_scan(const ScanArgs& args, int dtype, cudaStream_t s) {
+    ScanArgs a = args;
+    const size_t esz = dtype == 0 ? 4 : 2;
+    a.wide = (rows_on_16(a.u, a.su, a, esz) ? 1 : 0) | (rows_on_16(a.delta, a.sdt, a, esz) ? 2 : 0) |
+             (a.z && rows_on_16(a.z, a.sz, a, esz) ? 4 : 0) | (rows_on_16(a.out, a.so, a, esz) ? 8 : 0);
     return dtype == 0 ? dispatch<float>(a, s) : dispatch<__nv_bfloat16>(a, s);
 }
 

@@ -75,6 +75,14 @@ __global__ void __launch_bounds__(kWarps * 32) scan_bwd_kernel(const ScanBwdArgs
 
     const int r = a.dim / a.groups;
     const int ct = blockIdx.x % (a.groups * a.tiles), g = ct / a.tiles, tile = ct % a.tiles;
+    each_rest_row(a.s, blockIdx.x / (a.groups * a.tiles), a.s.n_seq, [&](long long row) {
+        const int k = tile * CH + threadIdx.x;
+        if (threadIdx.x < CH && k < r) {
+            const long long at = row * a.dim + g * r + k;
+            static_cast<T*>(a.du)[at] = static_cast<T*>(a.ddelta)[at] = from_f32<T>(0.f);
+            if (a.dz) static_cast<T*>(a.dz)[at] = from_f32<T>(0.f);
+        }
+    });
     Piece p;
     find_piece(a.s, blockIdx.x / (a.groups * a.tiles), 1 << 30, p);  // the whole sequence
 
@@ -265,12 +273,14 @@ __global__ void __launch_bounds__(256) scan_bwd_sum_kernel(const ScanBwdArgs a, 
     const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
     if (i < n_bc) {
         const long long per = rows * a.groups * 2 * a.N, row = i / (a.groups * 2 * a.N);
-        if (a.s.cu) {  // rows outside every sequence stay as they were
-            const long long lo = cu_at(a.s.cu, 0, a.s.L), hi = cu_at(a.s.cu, a.s.n_seq, a.s.L);
-            if (row < lo || row >= hi) return;
+        bool in = true;
+        if (a.s.cu) {
+            in = row >= cu_at(a.s.cu, 0, a.s.L) && row < cu_at(a.s.cu, a.s.n_seq, a.s.L);
+            if (!in && !a.s.zero_rest) return;
         }
         float s = 0.f;
-        for (int k = 0; k < a.tiles; ++k) s += a.part_bc[k * per + i];
+        if (in)
+            for (int k = 0; k < a.tiles; ++k) s += a.part_bc[k * per + i];
         const int n = static_cast<int>(i % a.N), which = static_cast<int>(i / a.N % 2);
         const long long g = i / (2 * a.N);
         (which ? static_cast<T*>(a.dC) : static_cast<T*>(a.dB))[g * a.N + n] = from_f32<T>(s);
@@ -315,6 +325,8 @@ cudaError_t dispatch(const ScanBwdArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
+
+int scan_bwd_channels(int N) { return kWarps * 32 / (N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16); }
 
 cudaError_t launch_scan_bwd(const ScanBwdArgs& a, int dtype, cudaStream_t s) {
     return dtype == 0 ? dispatch<float>(a, s) : dispatch<__nv_bfloat16>(a, s);

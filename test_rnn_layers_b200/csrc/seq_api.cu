@@ -28,6 +28,8 @@ int check_shape(int n_seq, long long L, int dim, int dtype) {
     return TTT_OK;
 }
 
+int min_of(int a, int b) { return a < b ? a : b; }
+
 size_t elem(int dtype) { return dtype == TTT_F32 ? 4 : 2; }
 
 // The strides of an operand: the caller's (batch, token), or those of contiguous rows of `width`.
@@ -46,7 +48,7 @@ int check_stride(const char* name, RowStride r, bool packed, int n_seq, long lon
     const long long big = 1ll << 50;
     if (r.t < 0 || r.t > big || (!packed && (r.b < 0 || r.b > big)))
         return fail(TTT_ERR_ARG, "%s: strides must be in [0, 2^50] (got %lld, %lld)", name, r.b, r.t);
-    if (!output) return TTT_OK;
+    if (!output || L == 0) return TTT_OK;
     const bool one_b = packed || n_seq == 1, one_t = L <= 1;
     bool apart = (one_t || r.t >= width) && (one_b || r.b >= width);
     if (apart && !one_b && !one_t) apart = r.b >= (L - 1) * r.t + width || r.t >= (n_seq - 1) * r.b + width;
@@ -78,7 +80,7 @@ int check_conv(int n_seq, long long L, int D, int width, int dtype, unsigned int
     TTT_TRY(check_shape(n_seq, L, D, dtype));
     if (width < 1) return fail(TTT_ERR_ARG, "width must be >= 1 (got %d)", width);
     if (width < 2 || width > 4) return fail(TTT_ERR_UNSUPPORTED, "only filter widths 2 to 4 are supported (got %d)", width);
-    if (flags & ~TTT_FLAG_SILU) return fail(TTT_ERR_ARG, "unknown flags 0x%x", flags);
+    if (flags & ~(TTT_FLAG_SILU | TTT_FLAG_ZERO_REST)) return fail(TTT_ERR_ARG, "unknown flags 0x%x", flags);
     return TTT_OK;
 }
 
@@ -95,13 +97,18 @@ int check_scan(int n_seq, long long L, int dim, int groups, int N, int dtype, un
     if (groups < 1 || dim % groups) return fail(TTT_ERR_ARG, "groups (%d) must divide dim (%d)", groups, dim);
     if (N < 1) return fail(TTT_ERR_ARG, "d_state must be >= 1 (got %d)", N);
     if (N > kMaxStates) return fail(TTT_ERR_UNSUPPORTED, "d_state up to %d is supported (got %d)", kMaxStates, N);
-    if (flags & ~TTT_FLAG_SOFTPLUS) return fail(TTT_ERR_ARG, "unknown flags 0x%x", flags);
-    const int ch = ttt::scan_channels(N), r = dim / groups;
+    if (flags & ~(TTT_FLAG_SOFTPLUS | TTT_FLAG_ZERO_REST)) return fail(TTT_ERR_ARG, "unknown flags 0x%x", flags);
+    const int ch = min_of(ttt::scan_channels(N), ttt::scan_bwd_channels(N)), r = dim / groups;
     return check_grid(slot_count(true, n_seq, L, 16) * groups * ((r + ch - 1) / ch));
 }
 
-// Into how many tokens a block's span is cut: whole sequences (split = false) where they fill the
-// GPU.
+// Whether the sequences are cut into spans of tokens, and how long those are.
+//
+// An SM holds two blocks.  Measured at N = 16 (64 channels a block): a token takes a block 0.11 us
+// alone on its SM and 0.17 us beside another, so whole sequences take longest * 0.11 (or 0.17) us, and
+// the rate of the full GPU is 2 * 148 / 0.17 = 1720 channel tiles a us and token.  Cutting costs about
+// 1.7 times the work, but runs at that rate: 2 sequences of 2048 tokens and 2048 channels take 226 us
+// whole and 160 us in spans, 4 of them 228 and 290 us, one of 8200 tokens 900 and 290 us.
 struct Split {
     bool on;
     int span;
@@ -112,17 +119,20 @@ Split scan_split(int n_seq, long long L, long long longest, bool packed, int dim
     const long long tiles = static_cast<long long>(groups) * ((r + ch - 1) / ch);
     const int whole = static_cast<int>((L + 16) / 16 * 16);  // past every token
     Split s{false, whole, n_seq};
-    const long long blocks = tiles * n_seq, want = 4 * kSms;
-    if (blocks < 2 * kSms && longest >= 256) {
-        const long long total = packed ? L : n_seq * L;
-        long long span = (total * tiles + want - 1) / want;
-        span = (span < 64 ? 64 : span) / 16 * 16;
-        if (span * 2 <= longest) {
-            s.on = true;
-            s.span = static_cast<int>(span);
-            s.slots = slot_count(packed, n_seq, L, span);
-        }
-    }
+    const long long blocks = tiles * n_seq, total = packed ? L : n_seq * L, slots = 2 * kSms;
+    const double t_whole = longest * (blocks <= kSms ? 0.11 : 0.17), t_split = 1.7 * total * tiles / 1720.0 + 10.0;
+    if (blocks >= slots || t_split >= t_whole) return s;
+    // two rounds of blocks, each full: 2 * slots blocks in all
+    long long per_tile = 2 * slots / tiles;
+    if (packed) per_tile -= n_seq / 2;  // a sequence's last span is half empty on average
+    long long spans = packed ? per_tile : per_tile / n_seq;
+    if (spans < 1) spans = 1;
+    long long span = ((packed ? total : L) + spans - 1) / spans;
+    span = ((span < 64 ? 64 : span) + 15) / 16 * 16;
+    if (span * 2 > longest) return s;
+    s.on = true;
+    s.span = static_cast<int>(span);
+    s.slots = slot_count(packed, n_seq, L, span);
     return s;
 }
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -163,7 +173,7 @@ int ttt_causal_conv_forward(const void* x, const float* weight, const float* bia
     TTT_TRY(check_aliasing(in, 6, outs, 2, same_ok, 1));
     if (L == 0 && !state_out) return ok();
     ttt::ConvArgs a{};
-    a.s = SeqShape{cu_seqlens, n_seq, L};
+    a.s = SeqShape{cu_seqlens, n_seq, L, packed && (flags & TTT_FLAG_ZERO_REST)};
     a.x = x; a.sx = sx; a.weight = weight; a.bias = bias; a.state_in = state_in; a.state_out = state_out;
     a.pages = pages; a.n_pages = n_pages; a.D = dim; a.W = width; a.silu = (flags & TTT_FLAG_SILU) != 0;
     a.out = out; a.so = so;
@@ -192,7 +202,7 @@ int ttt_causal_conv_step(const void* x, const float* weight, const float* bias, 
                          {"state", state, static_cast<size_t>(n_pages) * (width - 1) * dim * esz}};
     TTT_TRY(check_aliasing(in, 4, outs, 2));
     ttt::ConvArgs a{};
-    a.s = SeqShape{nullptr, n_seq, 1};
+    a.s = SeqShape{nullptr, n_seq, 1, false};
     a.x = x; a.sx = sx; a.weight = weight; a.bias = bias; a.state_out = state;
     a.pages = pages; a.n_pages = n_pages; a.D = dim; a.W = width; a.silu = (flags & TTT_FLAG_SILU) != 0;
     a.out = out; a.so = so;
@@ -249,7 +259,7 @@ int ttt_causal_conv_backward(const void* x, const float* weight, const float* bi
                          {"d_state_in", d_state_in, st}, {"workspace", workspace, static_cast<size_t>(bytes)}};
     TTT_TRY(check_aliasing(in, 7, outs, 5));
     ttt::ConvBwdArgs a{};
-    a.s = SeqShape{cu_seqlens, n_seq, L};
+    a.s = SeqShape{cu_seqlens, n_seq, L, packed && (flags & TTT_FLAG_ZERO_REST)};
     a.x = x; a.sx = sx; a.weight = weight; a.bias = bias; a.state_in = state_in; a.d_out = d_out; a.sd = sd;
     a.d_state_out = d_state_out; a.D = dim; a.W = width; a.silu = (flags & TTT_FLAG_SILU) != 0;
     a.dx = dx; a.d_state_in = d_state_in; a.d_weight = d_weight; a.d_bias = d_bias;
@@ -335,7 +345,7 @@ int ttt_selective_scan_forward(const void* u, const void* delta, const float* A,
     const long long longest = packed && max_seqlen > 0 && max_seqlen < L ? max_seqlen : L;
     const Split sp = scan_split(n_seq, L, longest, packed, dim, groups, d_state);
     ttt::ScanArgs a{};
-    a.s = SeqShape{cu_seqlens, n_seq, L};
+    a.s = SeqShape{cu_seqlens, n_seq, L, packed && (flags & TTT_FLAG_ZERO_REST)};
     a.u = u; a.delta = delta; a.B = B; a.C = C; a.z = z;
     a.su = su; a.sdt = sdt; a.sB = sB; a.sC = sC; a.sz = sz; a.so = so;
     a.A = A; a.D = D; a.bias = delta_bias; a.dim = dim; a.groups = groups; a.N = d_state;
@@ -397,7 +407,7 @@ long long ttt_selective_scan_backward_workspace_bytes(int n_seq, long long L, in
     const int rc = check_scan(n_seq, L, dim, groups, d_state, TTT_F32, 0);
     if (rc) return rc;
     ok();
-    const int ch = ttt::scan_channels(d_state), tiles = (dim / groups + ch - 1) / ch;
+    const int ch = ttt::scan_bwd_channels(d_state), tiles = (dim / groups + ch - 1) / ch;
     const size_t rows = static_cast<size_t>(packed ? L : n_seq * L);
     return static_cast<long long>(up256(tiles * rows * groups * 2 * d_state * 4) +
                                   up256(static_cast<size_t>(n_seq) * dim * d_state * 4) +
@@ -457,7 +467,7 @@ int ttt_selective_scan_backward(const void* u, const void* delta, const float* A
                          {"d_state_in", d_state_in, n_seq * state}, {"workspace", workspace, static_cast<size_t>(bytes)}};
     TTT_TRY(check_aliasing(in, 12, outs, 10));
     ttt::ScanBwdArgs a{};
-    a.s = SeqShape{cu_seqlens, n_seq, L};
+    a.s = SeqShape{cu_seqlens, n_seq, L, packed && (flags & TTT_FLAG_ZERO_REST)};
     a.u = u; a.delta = delta; a.B = B; a.C = C; a.z = z; a.d_out = d_out;
     a.su = su; a.sdt = sdt; a.sB = sB; a.sC = sC; a.sz = sz; a.sdo = sdo;
     a.A = A; a.D = D; a.bias = delta_bias; a.dim = dim; a.groups = groups; a.N = d_state;
@@ -465,7 +475,7 @@ int ttt_selective_scan_backward(const void* u, const void* delta, const float* A
     a.ckpt = ckpt; a.d_state_out = d_state_out;
     a.du = du; a.ddelta = d_delta; a.dB = dB; a.dC = dC; a.dz = dz; a.dA = dA; a.dD = dD; a.dbias = d_delta_bias;
     a.d_state_in = d_state_in;
-    const int ch = ttt::scan_channels(d_state);
+    const int ch = ttt::scan_bwd_channels(d_state);
     a.tiles = (dim / groups + ch - 1) / ch;
     char* w = static_cast<char*>(workspace);
     a.part_bc = reinterpret_cast<float*>(w);

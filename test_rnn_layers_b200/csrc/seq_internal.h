@@ -14,6 +14,7 @@ struct SeqShape {
     const int* cu;
     int n_seq;
     long long L;
+    bool zero_rest;           // packed: rows outside every sequence are written as zeros
 };
 
 // Element strides of a tensor's batch rows and tokens (channels are contiguous).
@@ -75,6 +76,7 @@ struct ScanArgs {
     float* seg_h;                // [n_slots][dim][N]: each span's own end state
     float* seg_dt;               // [n_slots][dim]: each span's sum of delta
     float* seg_h0;               // [n_seq][dim][N]: the start states
+    int wide;                    // bits 0 .. 3: the rows of u, delta, z, out start on 16-byte boundaries
 };
 constexpr int kScanChunk = 8;    // tokens between the states a training forward keeps
 
@@ -129,7 +131,8 @@ cudaError_t launch_conv_step(const ConvArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_conv_bwd(const ConvBwdArgs& a, int dtype, cudaStream_t s);
 int conv_bwd_span(int n_seq, long long L, bool packed, int D, int dtype);
 
-int scan_channels(int N);        // channels per block of the scan kernels
+int scan_channels(int N);        // channels per block of the scan kernel
+int scan_bwd_channels(int N);    // and of its gradient's
 cudaError_t launch_scan(const ScanArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_scan_step(const ScanStepArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_scan_bwd(const ScanBwdArgs& a, int dtype, cudaStream_t s);

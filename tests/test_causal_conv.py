@@ -134,10 +134,10 @@ def test_steps_continue_a_prompt(libttt, D, W, dt):
     assert torch.equal(torch.cat(out, 1), whole) and torch.equal(part, end)
 
 
-def test_step_without_a_page_leaves_its_row(libttt):
+def test_step_without_a_page_gives_zeros(libttt):
     x, w, b, pool, _ = inputs(3, 1, 16, 4, torch.bfloat16, 37)
     out, before = torch.full((3, 16), 5.0, device="cuda").bfloat16(), pool.clone()
     libttt.ttt_causal_conv_step(x[:, 0], pool, w, b, pages=torch.tensor([1, -1, 99], dtype=torch.int32, device="cuda"), out=out)
-    assert (out[1:] == 5).all() and (out[0] != 5).any()
+    assert (out[1:] == 0).all() and (out[0] != 5).any()
     keep = [0, 2, 3, 4, 5]
     assert torch.equal(pool[keep], before[keep]) and not torch.equal(pool[1], before[1])

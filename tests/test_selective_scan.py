@@ -202,13 +202,13 @@ def test_steps_continue_a_prompt(libttt, D, N, G, dt):
     ref.check("state", pool[pages.long()], torch.stack(want.last), torch.stack(want.last_mag), want.c, torch.float32)
 
 
-def test_step_without_a_page_leaves_its_row(libttt):
+def test_step_without_a_page_gives_zeros(libttt):
     s = inputs((3,), 16, 16, 1, torch.bfloat16, 37)
     a, k = positional(s)
     pool = torch.randn(4, 16, 16, device="cuda")
     out, before = torch.full((3, 16), 5.0, device="cuda").bfloat16(), pool.clone()
     libttt.ttt_selective_scan_step(*a, pool, **k, pages=torch.tensor([1, -1, 99], dtype=torch.int32, device="cuda"), out=out)
-    assert (out[1:] == 5).all() and (out[0] != 5).any()
+    assert (out[1:] == 0).all() and (out[0] != 5).any()
     assert torch.equal(pool[[0, 2, 3]], before[[0, 2, 3]]) and not torch.equal(pool[1], before[1])
 
 
