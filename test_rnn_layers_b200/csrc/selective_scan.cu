@@ -32,75 +32,6 @@ constexpr int kTile = 16;
 
 enum Mode { kSpanState, kOut, kOutGated };
 
-// The S states of a lane, of which the last lanes may hold fewer (`left`) when PAD.
-template <int S, bool PAD>
-__device__ __forceinline__ void load_state(const float* p, int left, float (&h)[S]) {
-    if constexpr (PAD) {
-#pragma unroll
-        for (int i = 0; i < S; ++i) h[i] = i < left ? p[i] : 0.f;
-    } else if constexpr (S == 2) {
-        load_vec<2>(p, h);
-    } else {
-#pragma unroll
-        for (int i = 0; i < S; i += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(p + i);
-            h[i] = v.x; h[i + 1] = v.y; h[i + 2] = v.z; h[i + 3] = v.w;
-        }
-    }
-}
-template <int S, bool PAD>
-__device__ __forceinline__ void store_state(float* p, int left, const float (&h)[S]) {
-    if constexpr (PAD) {
-#pragma unroll
-        for (int i = 0; i < S; ++i)
-            if (i < left) p[i] = h[i];
-    } else if constexpr (S == 2) {
-        store_vec<2>(p, h);
-    } else {
-#pragma unroll
-        for (int i = 0; i < S; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
-    }
-}
-template <int S, bool PAD>
-__device__ __forceinline__ void load_state(const float* p, int left, f32x2 (&h)[S / 2]) {
-    float v[S];
-    load_state<S, PAD>(p, left, v);
-#pragma unroll
-    for (int i = 0; i < S / 2; ++i) h[i] = pack2(v[2 * i], v[2 * i + 1]);
-}
-template <int S, bool PAD>
-__device__ __forceinline__ void store_state(float* p, int left, const f32x2 (&h)[S / 2]) {
-    float v[S];
-#pragma unroll
-    for (int i = 0; i < S / 2; ++i) unpack2(h[i], v[2 * i], v[2 * i + 1]);
-    store_state<S, PAD>(p, left, v);
-}
-
-// S floats of shared memory as pairs.
-template <int S>
-__device__ __forceinline__ void load_pairs(const float* p, f32x2 (&v)[S / 2]) {
-    if constexpr (S == 2) {
-        v[0] = *reinterpret_cast<const f32x2*>(p);
-    } else {
-#pragma unroll
-        for (int i = 0; i < S / 2; i += 2) {
-            const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(p + 2 * i);
-            v[i] = t.x; v[i + 1] = t.y;
-        }
-    }
-}
-
-__device__ __forceinline__ void cp_async_16(void* smem, const void* gmem) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-// Layout of the lanes: P lanes a channel with S states each, R channels a lane, NW warps a block.
-template <int S_, int P_, int R_, int NW_>
-struct Lanes {
-    static constexpr int S = S_, P = P_, R = R_, NW = NW_, CPW = 32 / P, CH = NW * CPW * R, NP = S * P, THREADS = NW * 32;
-};
-
 // The layouts, by the number of states N.  Four states a lane and one channel a lane for N = 16: two
 // channels a lane read B and C half as often but leave 1.7 warps for each scheduler at the sizes of a
 // training batch, eight states a lane likewise (8 x 2048 tokens, 2048 channels: 353 us against 389 and

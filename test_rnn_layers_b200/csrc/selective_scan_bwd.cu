@@ -9,264 +9,408 @@
 //   du_t   = D dy_t + dt_t sum_n dh_t B_t,   dz_t = d_out_t y_t silu'(z_t),   dD = sum dy_t u_t.
 //
 // The states h_t are needed from the last token back, so the forward keeps the state before every
-// kScanChunk-th token; a block takes one sequence and a tile of channels (laid out over the lanes as
-// in the forward), goes through the chunks from the last one, computes a chunk's 8 states and decay
-// factors again in registers, and then steps back through them.  The sums over the channels of dB
-// and dC are taken over a warp's channels by shuffles, over the block's warps in shared memory, and
-// over the blocks of a group by a second kernel, in a fixed order; dA, dD and d bias are summed over
-// the tokens in registers and over the sequences by that kernel too.
+// kScanChunk-th token; a block takes one sequence (or a span of one) and a tile of channels, laid out
+// over the lanes as in the forward, goes through the chunks from the last one, computes a chunk's 8
+// states and decay factors again in registers, and then steps back through them.
+//
+// What bounds it is the shared-memory pipe and issue, not the bytes: each value a lane reads from
+// shared memory or a neighbour costs a pass of the pipe, and dB and dC have to be summed over the
+// channels, which are other lanes.  So a lane takes R = 2 channels one after the other and adds their
+// shares of dB and dC up in registers: B and C are read and the shares summed over the warp half as
+// often.  The sums over the block's warps go through shared memory, those over the blocks of a group
+// and over the sequences through a second kernel, all in a fixed order.
+//
+// Few long sequences are cut into spans as in the forward: a first launch finds what each span passes
+// back to the one before it, starting from nothing, and the main one starts each span from
+//   dh = (own part of the next span) + exp(A sum dt of it) (dh behind it).
 #include "seq_common.cuh"
 
 namespace ttt {
 namespace {
 
-constexpr int kWarps = 8;
 constexpr int kT = kScanChunk;
 
-template <bool PAD>
-__device__ __forceinline__ void load4(const float* p, int left, float (&h)[4]) {
-    if constexpr (!PAD) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        h[0] = v.x; h[1] = v.y; h[2] = v.z; h[3] = v.w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = i < left ? p[i] : 0.f;
-    }
-}
-template <bool PAD>
-__device__ __forceinline__ void store4(float* p, int left, const float (&h)[4]) {
-    if constexpr (!PAD) {
-        *reinterpret_cast<float4*>(p) = make_float4(h[0], h[1], h[2], h[3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < left) p[i] = h[i];
-    }
+// The sums over a channel's P lanes of P values (P <= kT; lane q ends with value q) or of kT values
+// (P = 2 kT; value q mod kT).
+template <int P, int CPW, int G>
+__device__ __forceinline__ float lane_sums(float (&v)[G], int q) {
+    const float s = reduce_across<G, CPW>(v, q);
+    return P > G ? s + __shfl_xor_sync(0xffffffffu, s, G * CPW) : s;
 }
 
-// The sums over a channel's P lanes of kT values (one a token): lane q ends with those of its tokens
-// q, P + q, ... (P <= kT) or, with P = 2 kT lanes, of token q mod kT.
-template <int P, int CPW>
-__device__ __forceinline__ void token_sums(float (&v)[kT], int q, float (&out)[(kT + P - 1) / P]) {
-    if constexpr (P <= kT) {
+// The sums over CPW neighbouring lanes of M values a lane: lane c ends with the M / CPW values from
+// M / CPW * c on, in v[0 ..].
+template <int M, int W, int TOTAL>
+__device__ __forceinline__ void channel_sums(float (&v)[TOTAL], int c) {
+    if constexpr (W >= 1) {
 #pragma unroll
-        for (int k = 0; k < kT / P; ++k) {
-            float w[P];
-#pragma unroll
-            for (int j = 0; j < P; ++j) w[j] = v[k * P + j];
-            out[k] = reduce_across<P, CPW>(w, q);
+        for (int i = 0; i < M / 2; ++i) {
+            const float send = (c & W) ? v[i] : v[i + M / 2], keep = (c & W) ? v[i + M / 2] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, W);
         }
-    } else {
-        const float s = reduce_across<kT, CPW>(v, q);
-        out[0] = s + __shfl_xor_sync(0xffffffffu, s, kT * CPW);
+        channel_sums<M / 2, W / 2>(v, c);
     }
 }
 
-template <typename T, int P, bool PAD>
-__global__ void __launch_bounds__(kWarps * 32) scan_bwd_kernel(const ScanBwdArgs a) {
-    constexpr int CPW = 32 / P, CH = kWarps * CPW, NP = 4 * P;
+template <typename T, class Y, bool PAD, bool GATE, bool SPAN>
+__global__ void __launch_bounds__(Y::THREADS) scan_bwd_kernel(const ScanBwdArgs a) {
+    // SPAN: the first launch of spans, which finds a span's own adjoint of its start state only.
+    constexpr int S = Y::S, P = Y::P, R = Y::R, NW = Y::NW, CPW = Y::CPW, CH = Y::CH, NP = Y::NP, TH = Y::THREADS;
+    static_assert(S == 4, "a chunk's 2 kT S shares are 64 values");
     constexpr int K = (kT + P - 1) / P;              // tokens of a chunk that a lane finishes
     constexpr int BC = kT * 2 * NP;                  // values of B and C of a chunk
-    constexpr int NB = (BC + kWarps * 32 - 1) / (kWarps * 32);
-    constexpr int V = 64 / CPW;                      // of a lane's 2 kT 4 shares, those it sums over the channels
-    __shared__ __align__(16) float sbc[BC];          // [token][B, C][n]
-    __shared__ __align__(16) float4 sv[kWarps][kT][CPW];  // (dt, dt u, dy)
-    __shared__ float red[kWarps][2][kT][NP];
+    constexpr int NB = (BC + TH - 1) / TH;
+    constexpr int V = 2 * kT * S / CPW;              // of a lane's shares, those it sums over the channels
+    constexpr int VE = 16 / sizeof(T);
+    constexpr int PIECES = kT * CH / VE;             // 16-byte pieces of a chunk of one operand
+    constexpr int ROW = CH + (CPW * sizeof(T) >= 16 ? CPW : VE);
+    constexpr int NRAW = GATE ? 4 : 3;               // u (du), delta (d delta), d_out, z (dz)
+    constexpr int EXTRA = P <= 8 ? 8 : 0;            // room for it up to 8 lanes a channel
+    __shared__ __align__(16) T raw[2][NRAW][kT][ROW];
+    __shared__ __align__(16) float sbc[2][BC];       // [token][B, C][n]
+    __shared__ __align__(16) float4 sh0[SPAN || PAD ? 1 : 2][SPAN || PAD ? 1 : R][SPAN || PAD ? 1 : TH];
+    // Rows padded so that the rows a warp writes at once lie in other banks.
+    __shared__ float2 sdt[NW][kT][R * CPW + EXTRA];  // (dt, dt u)
+    __shared__ float sdy[NW][kT][R * CPW + EXTRA];
+    __shared__ __align__(16) float red[SPAN ? 1 : 2][NW][2 * kT][NP + EXTRA / 2];  // [dB, dC][token][n]
 
     const int r = a.dim / a.groups;
-    const int ct = blockIdx.x % (a.groups * a.tiles), g = ct / a.tiles, tile = ct % a.tiles;
-    each_rest_row(a.s, blockIdx.x / (a.groups * a.tiles), a.s.n_seq, [&](long long row) {
-        const int k = tile * CH + threadIdx.x;
-        if (threadIdx.x < CH && k < r) {
-            const long long at = row * a.dim + g * r + k;
-            static_cast<T*>(a.du)[at] = static_cast<T*>(a.ddelta)[at] = from_f32<T>(0.f);
-            if (a.dz) static_cast<T*>(a.dz)[at] = from_f32<T>(0.f);
-        }
-    });
+    const int ct = blockIdx.x % (a.groups * a.tiles), g = ct / a.tiles, tile = ct % a.tiles, c0 = tile * CH;
+    const int slot = blockIdx.x / (a.groups * a.tiles);
+    if (!SPAN)
+        each_rest_row(a.s, slot, a.n_slots, [&](long long row) {
+            for (int k = threadIdx.x; k < CH; k += TH)
+                if (c0 + k < r) {
+                    const long long at = row * a.dim + g * r + c0 + k;
+                    static_cast<T*>(a.du)[at] = static_cast<T*>(a.ddelta)[at] = from_f32<T>(0.f);
+                    if (GATE) static_cast<T*>(a.dz)[at] = from_f32<T>(0.f);
+                }
+        });
     Piece p;
-    find_piece(a.s, blockIdx.x / (a.groups * a.tiles), 1 << 30, p);  // the whole sequence
+    const bool found = find_piece(a.s, slot, a.span, p);
+    if (SPAN && (!found || p.tile == 0)) return;     // nothing lies before a sequence's first span
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane / CPW, c = lane % CPW;
-    const int cg = tile * CH + warp * CPW + c;
-    const bool live = cg < r;
-    const int d = g * r + (live ? cg : r - 1);
-    const int left = a.N - 4 * q;
+    const int cb = warp * CPW * R + c;               // the lane's first channel within the block; the others CPW apart
+    const int left = a.N - S * q;
     const bool mine = P <= kT || q < kT;             // this lane finishes tokens
-    const long long hoff = static_cast<long long>(d) * a.N + 4 * q, hrow = static_cast<long long>(a.dim) * a.N;
-
-    float A[4], A2[4], dA[4] = {0.f, 0.f, 0.f, 0.f}, dh[4] = {0.f, 0.f, 0.f, 0.f};
-    load4<PAD>(a.A + hoff, left, A);
+    const long long hrow = static_cast<long long>(a.dim) * a.N;
+    bool live[R];
+    int d[R];
+    long long hoff[R];
+    f32x2 A2[R][S / 2], dA[R][S / 2], dh[R][S / 2];
+    float bias[R], Dk[R], sum_D[R] = {}, sum_bias[R] = {}, sum_dt[R] = {};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) A2[i] = A[i] * kLog2e;
-    if (a.d_state_out) load4<PAD>(a.d_state_out + p.b * hrow + hoff, left, dh);
-    const float bias = a.bias ? a.bias[d] : 0.f, Dk = a.D ? a.D[d] : 0.f;
-    float sum_D = 0.f, sum_bias = 0.f;
+    for (int m = 0; m < R; ++m) {
+        live[m] = c0 + cb + m * CPW < r;
+        d[m] = g * r + (live[m] ? c0 + cb + m * CPW : r - 1);
+        hoff[m] = static_cast<long long>(d[m]) * a.N + S * q;
+        load_state<S, PAD>(a.A + hoff[m], left, A2[m]);
+#pragma unroll
+        for (int i = 0; i < S / 2; ++i) {
+            A2[m][i] = mul2(A2[m][i], both(kLog2e));
+            dA[m][i] = dh[m][i] = both(0.f);
+        }
+        bias[m] = a.bias ? a.bias[d[m]] : 0.f;
+        Dk[m] = a.D ? a.D[d[m]] : 0.f;
+    }
+    const int first = found ? p.tile * a.span : 0, last = found ? min(first + a.span, p.len) : 0;
+    if (!SPAN && found) {
+#pragma unroll
+        for (int m = 0; m < R; ++m) {
+            if (a.d_state_out && live[m]) load_state<S, PAD>(a.d_state_out + p.b * hrow + hoff[m], left, dh[m]);
+            const int spans = p.len > 0 ? (p.len + a.span - 1) / a.span : 1;
+            for (int s = p.slot + spans - 1 - p.tile; s > p.slot; --s) {  // the spans behind this one, from the last
+                f32x2 e[S / 2];
+                load_state<S, PAD>(a.seg_dh + s * hrow + hoff[m], left, e);
+                const float sum = a.seg_dt[static_cast<long long>(s) * a.dim + d[m]];
+#pragma unroll
+                for (int i = 0; i < S / 2; ++i) dh[m][i] = fma2(decay2(mul2(both(sum), A2[m][i])), dh[m][i], e[i]);
+            }
+        }
+    }
 
-    const T* u = static_cast<const T*>(a.u) + p.row * a.su.b + p.t0 * a.su.t + d;
-    const T* dl = static_cast<const T*>(a.delta) + p.row * a.sdt.b + p.t0 * a.sdt.t + d;
-    const T* z = a.z ? static_cast<const T*>(a.z) + p.row * a.sz.b + p.t0 * a.sz.t + d : nullptr;
-    const T* dout = static_cast<const T*>(a.d_out) + p.row * a.sdo.b + p.t0 * a.sdo.t + d;
+    const long long at0 = g * r + c0, row0 = p.row * a.s.L + p.t0;  // the block's channels; first row of the outputs
+    const T* u = static_cast<const T*>(a.u) + p.row * a.su.b + p.t0 * a.su.t + at0;
+    const T* dl = static_cast<const T*>(a.delta) + p.row * a.sdt.b + p.t0 * a.sdt.t + at0;
+    const T* z = static_cast<const T*>(a.z) + p.row * a.sz.b + p.t0 * a.sz.t + at0;
+    const T* dout = static_cast<const T*>(a.d_out) + p.row * a.sdo.b + p.t0 * a.sdo.t + at0;
     const T* Bm = static_cast<const T*>(a.B) + p.row * a.sB.b + p.t0 * a.sB.t + g * a.N;
     const T* Cm = static_cast<const T*>(a.C) + p.row * a.sC.b + p.t0 * a.sC.t + g * a.N;
-    const long long row0 = p.row * a.s.L + p.t0;     // first row of the contiguous outputs
-    T* du = static_cast<T*>(a.du) + row0 * a.dim + d;
-    T* ddelta = static_cast<T*>(a.ddelta) + row0 * a.dim + d;
-    T* dz = a.dz ? static_cast<T*>(a.dz) + row0 * a.dim + d : nullptr;
     const long long rows = a.s.cu ? a.s.L : a.s.n_seq * a.s.L;
     float* part_bc = a.part_bc + ((tile * rows + row0) * a.groups + g) * 2 * a.N;
     const long long chunk0 = a.s.cu ? slot_base(a.s.cu, p.b, a.s.L, kT) : p.b * ((a.s.L + kT - 1) / kT);
-    const float* ckpt = a.ckpt + chunk0 * hrow + hoff;
+    const float* ckpt = a.ckpt + chunk0 * hrow;
 
-    T ru[K], rd[K], rz[K], ro[K], rbc[NB];
-    float h0[4];
-    auto load_chunk = [&](int ch) {
-        const int t0 = ch * kT;
+    T rbc[NB];
+    auto fetch = [&](T* to, const T* from, bool wide, int ch) {
+        if (wide) {
+            cp_async_16(to, from);
+        } else {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int t = t0 + k * P + q;
-            ru[k] = rd[k] = rz[k] = ro[k] = from_f32<T>(0.f);
-            if (mine && t < p.len) {
-                ru[k] = u[t * a.su.t];
-                rd[k] = dl[t * a.sdt.t];
-                ro[k] = dout[t * a.sdo.t];
-                if (z) rz[k] = z[t * a.sz.t];
+            for (int i = 0; i < VE; ++i)
+                if (c0 + ch + i < r) to[i] = from[i];
+        }
+    };
+    auto load_chunk = [&](int buf, int t0) {
+        for (int e = threadIdx.x; e < PIECES; e += TH) {
+            const int t = e / (CH / VE), ch = e % (CH / VE) * VE;
+            if (t0 + t < last) {
+                const bool in = c0 + ch + VE <= r;
+                if (!SPAN) fetch(&raw[buf][0][t][ch], u + (t0 + t) * a.su.t + ch, in && (a.wide & 1), ch);
+                fetch(&raw[buf][1][t][ch], dl + (t0 + t) * a.sdt.t + ch, in && (a.wide & 2), ch);
+                fetch(&raw[buf][2][t][ch], dout + (t0 + t) * a.sdo.t + ch, in && (a.wide & 8), ch);
+                if (GATE) fetch(&raw[buf][GATE ? 3 : 0][t][ch], z + (t0 + t) * a.sz.t + ch, in && (a.wide & 4), ch);
             }
+        }
+        if constexpr (!SPAN && !PAD) {
+#pragma unroll
+            for (int m = 0; m < R; ++m) cp_async_16(&sh0[buf][m][threadIdx.x], ckpt + t0 / kT * hrow + hoff[m]);
         }
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            const int e = k * kWarps * 32 + threadIdx.x, t = t0 + e / (2 * NP), n = e % NP;
+            const int e = k * TH + threadIdx.x, t = t0 + e / (2 * NP), n = e % NP;
             rbc[k] = from_f32<T>(0.f);
-            if (e < BC && t < p.len && (!PAD || n < a.N))
+            if (e < BC && t < last && (!PAD || n < a.N))
                 rbc[k] = (e / NP) & 1 ? Cm[t * a.sC.t + n] : Bm[t * a.sB.t + n];
         }
-        load4<PAD>(ckpt + ch * hrow, left, h0);
     };
-
-    const int chunks = (p.len + kT - 1) / kT;
-    if (chunks > 0) load_chunk(chunks - 1);
-    for (int ch = chunks - 1; ch >= 0; --ch) {
-        const int t0 = ch * kT, n = min(kT, p.len - t0);
+    // What a finished chunk leaves in shared memory: its outputs, and the warps' shares of dB and dC.
+    auto store_chunk = [&](int buf, int t0) {
+        for (int e = threadIdx.x; e < PIECES; e += TH) {
+            const int t = e / (CH / VE), ch = e % (CH / VE) * VE;
+            if (t0 + t < last) {
+                const long long at = (row0 + t0 + t) * a.dim + at0 + ch;
+                auto put = [&](void* base, int k, bool wide) {
+                    const T* from = &raw[buf][k][t][ch];
+                    T* to = static_cast<T*>(base) + at;
+                    if (wide && c0 + ch + VE <= r) {
+                        *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+                    } else {
 #pragma unroll
-        for (int k = 0; k < NB; ++k) {
-            const int e = k * kWarps * 32 + threadIdx.x;
-            if (e < BC) sbc[e] = to_f32(rbc[k]);
-        }
-        float fu[K], fz[K], fo[K], fdy[K], fx[K], fdt[K], hs[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) hs[i] = h0[i];
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            fu[k] = to_f32(ru[k]);
-            fz[k] = to_f32(rz[k]);
-            fo[k] = to_f32(ro[k]);
-            fx[k] = to_f32(rd[k]) + bias;
-            fdt[k] = a.softplus ? softplus_f(fx[k]) : fx[k];
-            if (k * P + q >= n) fdt[k] = 0.f;
-            fdy[k] = z ? fo[k] * silu_f(fz[k]) : fo[k];
-            if (mine) sv[warp][k * P + q][c] = make_float4(fdt[k], fdt[k] * fu[k], fdy[k], 0.f);
-        }
-        __syncthreads();  // B, C and the tokens' values; the last chunk's sums have been read
-        if (ch > 0) load_chunk(ch - 1);
-
-        // the chunk's decay factors and states
-        float av[kT][4], hv[kT][4], y[kT], s1[kT], s2[kT];
-#pragma unroll
-        for (int t = 0; t < kT; ++t) {
-            const float4 v = sv[warp][t][c];
-            const float4 b4 = *reinterpret_cast<const float4*>(&sbc[(2 * t) * NP + 4 * q]);
-            const float4 c4 = *reinterpret_cast<const float4*>(&sbc[(2 * t + 1) * NP + 4 * q]);
-            const float b[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                av[t][i] = decay2(t < n ? v.x * A2[i] : 0.f);
-                hv[t][i] = fmaf(av[t][i], t ? hv[t - 1][i] : hs[i], v.y * b[i]);
-                if (PAD && i >= left) hv[t][i] = 0.f;
-            }
-            y[t] = fmaf(c4.x, hv[t][0], c4.y * hv[t][1]) + fmaf(c4.z, hv[t][2], c4.w * hv[t][3]);
-        }
-        // back through it
-        float share[64];  // [dB, dC][token][n]
-#pragma unroll
-        for (int t = kT - 1; t >= 0; --t) {
-            const float4 v = sv[warp][t][c];
-            const float4 b4 = *reinterpret_cast<const float4*>(&sbc[(2 * t) * NP + 4 * q]);
-            const float4 c4 = *reinterpret_cast<const float4*>(&sbc[(2 * t + 1) * NP + 4 * q]);
-            const float b[4] = {b4.x, b4.y, b4.z, b4.w}, cc[4] = {c4.x, c4.y, c4.z, c4.w};
-            s1[t] = s2[t] = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float e = fmaf(v.z, cc[i], dh[i]);
-                share[(kT + t) * 4 + i] = live ? v.z * hv[t][i] : 0.f;
-                share[t * 4 + i] = live ? e * v.y : 0.f;
-                dh[i] = e * av[t][i];
-                const float m = dh[i] * (t ? hv[t - 1][i] : hs[i]);
-                s1[t] = fmaf(e, b[i], s1[t]);
-                s2[t] = fmaf(m, A[i], s2[t]);
-                dA[i] = fmaf(m, v.x, dA[i]);
+                        for (int i = 0; i < VE; ++i)
+                            if (c0 + ch + i < r) to[i] = from[i];
+                    }
+                };
+                put(a.du, 0, a.wide & 16);
+                put(a.ddelta, 1, a.wide & 32);
+                if (GATE) put(a.dz, GATE ? 3 : 0, a.wide & 64);
             }
         }
-        float ys[K], s1s[K], s2s[K];
-        token_sums<P, CPW>(s1, q, s1s);
-        token_sums<P, CPW>(s2, q, s2s);
-        if (z) token_sums<P, CPW>(y, q, ys);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int t = k * P + q;
-            if (mine && t < n) {
-                const float gd = fmaf(fu[k], s1s[k], s2s[k]);
-                const float gx = a.softplus ? gd * sigmoid_f(fx[k]) : gd;
-                sum_bias += gx;
-                sum_D = fmaf(fdy[k], fu[k], sum_D);
-                if (live) {
-                    const long long at = static_cast<long long>(t0 + t) * a.dim;
-                    du[at] = from_f32<T>(fmaf(Dk, fdy[k], fdt[k] * s1s[k]));
-                    ddelta[at] = from_f32<T>(gx);
-                    if (z) dz[at] = from_f32<T>(fo[k] * fmaf(Dk, fu[k], ys[k]) * silu_grad_f(fz[k], sigmoid_f(fz[k])));
-                }
-            }
-        }
-        // the shares of dB and dC over the warp's channels: lane c ends with the shares V c .. V c + V - 1
-#pragma unroll
-        for (int w = CPW / 2, m = 32; w >= 1; w /= 2, m /= 2) {
-#pragma unroll
-            for (int i = 0; i < m; ++i) {
-                const float send = (c & w) ? share[i] : share[i + m], keep = (c & w) ? share[i + m] : share[i];
-                share[i] = keep + __shfl_xor_sync(0xffffffffu, send, w);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = c * V + i;
-            (&red[warp][0][0][0])[(e / 4) * NP + 4 * q + e % 4] = share[i];
-        }
-        __syncthreads();
-        // and over the block's warps
-        for (int e = threadIdx.x; e < 2 * kT * NP; e += kWarps * 32) {
-            const int which = e / (kT * NP), t = e / NP % kT, nn = e % NP;
+        for (int e = threadIdx.x; e < 2 * kT * NP; e += TH) {
+            const int row = e / NP, which = row / kT, t = row % kT, nn = e % NP;
             float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) s += red[w][which][t][nn];
-            if (t < n && (!PAD || nn < a.N))
+            for (int w = 0; w < NW; ++w) s += red[SPAN ? 0 : buf][w][row][nn];
+            if (t0 + t < last && (!PAD || nn < a.N))
                 part_bc[(static_cast<long long>(t0 + t) * a.groups * 2 + which) * a.N + nn] = s;
         }
+    };
+
+    int buf = 0;
+    const int top = (last - first + kT - 1) / kT * kT + first - kT;  // first token of the last chunk
+    if (first < last) load_chunk(0, top);
+    for (int t0 = top; t0 >= first && first < last; t0 -= kT, buf ^= 1) {
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+            const int e = k * TH + threadIdx.x;
+            if (e < BC) sbc[buf][e] = to_f32(rbc[k]);
+        }
+        cp_async_wait();
+        __syncthreads();  // this chunk is there, and the one before (behind it in time) is done with
+        if (!SPAN && t0 < top) store_chunk(buf ^ 1, t0 + kT);
+        if (t0 - kT >= first) load_chunk(buf ^ 1, t0 - kT);
+
+        const int n = min(kT, last - t0);
+        // A token's values for the lane that finishes it; read again after the chunk, which needs the registers.
+        struct Token {
+            float u, x, dt, o, z, dy;
+        };
+        auto token = [&](int m, int k) {
+            const int t = k * P + q, ch = cb + m * CPW;
+            Token v{0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (mine && t < n && live[m]) {
+                if (!SPAN) v.u = to_f32(raw[buf][0][t][ch]);
+                v.x = to_f32(raw[buf][1][t][ch]) + bias[m];
+                v.dy = v.o = to_f32(raw[buf][2][t][ch]);
+                if (GATE) v.z = to_f32(raw[buf][GATE ? 3 : 0][t][ch]);
+            }
+            return v;
+        };
+#pragma unroll
+        for (int m = 0; m < R; ++m)
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int t = k * P + q;
+                const Token v = token(m, k);
+                float dt = a.softplus ? softplus_f(v.x) : v.x;
+                if (!(mine && t < n && live[m])) dt = 0.f;
+                if (SPAN) sum_dt[m] += dt;
+                if (mine) {
+                    sdt[warp][t][m * CPW + c] = make_float2(dt, dt * v.u);
+                    sdy[warp][t][m * CPW + c] = GATE ? v.o * silu_f(v.z) : v.o;
+                }
+            }
+        __syncwarp();
+
+        f32x2 sB[kT][S / 2], sC[kT][S / 2];           // the lane's shares of dB and dC
+        auto channel = [&](auto full, auto mm) {
+            constexpr bool FULL = decltype(full)::value;
+            constexpr int m = decltype(mm)::value;
+            f32x2 av[kT][S / 2], hv[kT][S / 2], h0[S / 2];
+            float ys[K], s1s[K], s2s[K];
+            // the chunk's decay factors and states
+#pragma unroll
+            for (int t = 0; t < kT; ++t) {
+                const f32x2 dt = both(sdt[warp][t][m * CPW + c].x);
+#pragma unroll
+                for (int i = 0; i < S / 2; ++i)
+                    av[t][i] = FULL || t < n ? decay2(mul2(dt, A2[m][i])) : both(1.f);
+            }
+            if constexpr (!SPAN) {
+                if constexpr (PAD) {
+                    load_state<S, PAD>(ckpt + t0 / kT * hrow + hoff[m], left, h0);
+                } else {
+                    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&sh0[buf][m][threadIdx.x]);
+                    h0[0] = v.x;
+                    h0[1] = v.y;
+                }
+                if (!live[m]) h0[0] = h0[1] = 0;
+#pragma unroll
+                for (int t = 0; t < kT; ++t) {
+                    f32x2 b[S / 2];
+                    load_pairs<S>(&sbc[buf][(2 * t) * NP + S * q], b);
+                    const f32x2 du2 = both(sdt[warp][t][m * CPW + c].y);
+#pragma unroll
+                    for (int i = 0; i < S / 2; ++i) {
+                        hv[t][i] = fma2(av[t][i], t ? hv[t - 1][i] : h0[i], mul2(du2, b[i]));
+                        if (PAD) {
+                            float lo, hi;
+                            unpack2(hv[t][i], lo, hi);
+                            hv[t][i] = pack2(2 * i < left ? lo : 0.f, 2 * i + 1 < left ? hi : 0.f);
+                        }
+                    }
+                }
+            }
+            // back through it; the sums over a channel's lanes for P tokens at a time
+            constexpr int G = P < kT ? P : kT;
+            float y[G], s1[G], s2[G];
+#pragma unroll
+            for (int t = kT - 1; t >= 0; --t) {
+                f32x2 b[S / 2], cc[S / 2], acc1 = 0, acc2 = 0, accy = 0;
+                load_pairs<S>(&sbc[buf][(2 * t + 1) * NP + S * q], cc);
+                if (!SPAN) load_pairs<S>(&sbc[buf][(2 * t) * NP + S * q], b);
+                const f32x2 dy2 = both(sdy[warp][t][m * CPW + c]);
+                const float2 v = sdt[warp][t][m * CPW + c];
+                const f32x2 dt2 = both(v.x), du2 = both(v.y);
+#pragma unroll
+                for (int i = 0; i < S / 2; ++i) {
+                    const f32x2 e = fma2(dy2, cc[i], dh[m][i]);
+                    dh[m][i] = mul2(e, av[t][i]);
+                    if (!SPAN) {
+                        const f32x2 w = mul2(dh[m][i], t ? hv[t - 1][i] : h0[i]);
+                        sC[t][i] = m ? fma2(dy2, hv[t][i], sC[t][i]) : mul2(dy2, hv[t][i]);
+                        sB[t][i] = m ? fma2(e, du2, sB[t][i]) : mul2(e, du2);
+                        acc1 = i ? fma2(e, b[i], acc1) : mul2(e, b[i]);
+                        acc2 = i ? fma2(w, A2[m][i], acc2) : mul2(w, A2[m][i]);
+                        dA[m][i] = fma2(w, dt2, dA[m][i]);
+                        if (GATE) accy = i ? fma2(cc[i], hv[t][i], accy) : mul2(cc[i], hv[t][i]);
+                    }
+                }
+                if (!SPAN) {
+                    float lo, hi;
+                    unpack2(acc1, lo, hi);
+                    s1[t % G] = lo + hi;
+                    unpack2(acc2, lo, hi);
+                    s2[t % G] = lo + hi;
+                    unpack2(accy, lo, hi);
+                    y[t % G] = lo + hi;
+                    if (t % G == 0) {
+                        s1s[t / G] = lane_sums<P, CPW>(s1, q);
+                        s2s[t / G] = lane_sums<P, CPW>(s2, q);
+                        if (GATE) ys[t / G] = lane_sums<P, CPW>(y, q);
+                    }
+                }
+            }
+            if constexpr (!SPAN) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const int t = k * P + q, ch = cb + m * CPW;
+                    if (mine && (FULL || t < n)) {
+                        const Token w = token(m, k);
+                        const float dt = sdt[warp][t][m * CPW + c].x, dy = sdy[warp][t][m * CPW + c];
+                        const float gd = fmaf(w.u, s1s[k], s2s[k] * 0.6931471805599453f);  // A2 = A log2(e)
+                        const float gx = a.softplus ? gd * sigmoid_f(w.x) : gd;
+                        if (live[m]) {
+                            sum_bias[m] += gx;
+                            sum_D[m] = fmaf(dy, w.u, sum_D[m]);
+                        }
+                        raw[buf][0][t][ch] = from_f32<T>(fmaf(Dk[m], dy, dt * s1s[k]));
+                        raw[buf][1][t][ch] = from_f32<T>(gx);
+                        if (GATE)
+                            raw[buf][GATE ? 3 : 0][t][ch] =
+                                from_f32<T>(w.o * fmaf(Dk[m], w.u, ys[k]) * silu_grad_f(w.z, sigmoid_f(w.z)));
+                    }
+                }
+            }
+        };
+        if (n == kT) {
+            channel(std::true_type{}, std::integral_constant<int, 0>{});
+            if constexpr (R == 2) channel(std::true_type{}, std::integral_constant<int, R - 1>{});
+        } else {
+            channel(std::false_type{}, std::integral_constant<int, 0>{});
+            if constexpr (R == 2) channel(std::false_type{}, std::integral_constant<int, R - 1>{});
+        }
+        if constexpr (!SPAN) {
+            float share[2 * kT * S];  // [dB, dC][token][n]
+#pragma unroll
+            for (int t = 0; t < kT; ++t)
+#pragma unroll
+                for (int i = 0; i < S / 2; ++i) {
+                    unpack2(sB[t][i], share[t * S + 2 * i], share[t * S + 2 * i + 1]);
+                    unpack2(sC[t][i], share[(kT + t) * S + 2 * i], share[(kT + t) * S + 2 * i + 1]);
+                }
+            channel_sums<2 * kT * S, CPW / 2>(share, c);
+            if constexpr (V % S == 0) {
+#pragma unroll
+                for (int i = 0; i < V; i += S)
+                    *reinterpret_cast<float4*>(&red[buf][warp][(c * V + i) / S][S * q]) =
+                        make_float4(share[i], share[i + 1], share[i + 2], share[i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) red[buf][warp][(c * V + i) / S][S * q + (c * V + i) % S] = share[i];
+            }
+        }
+    }
+    if (!SPAN && first < last) {
+        __syncthreads();
+        store_chunk(buf ^ 1, first);
     }
 #pragma unroll
-    for (int w = P / 2; w >= 1; w /= 2) {
-        sum_D += __shfl_xor_sync(0xffffffffu, sum_D, w * CPW);
-        sum_bias += __shfl_xor_sync(0xffffffffu, sum_bias, w * CPW);
-    }
-    if (live) {
-        store4<PAD>(a.part_a + p.b * hrow + hoff, left, dA);
-        if (a.d_state_in) store4<PAD>(a.d_state_in + p.b * hrow + hoff, left, dh);
-        if (q == 0) {
-            a.part_d[(2ll * p.b) * a.dim + d] = sum_D;
-            a.part_d[(2ll * p.b + 1) * a.dim + d] = sum_bias;
+    for (int m = 0; m < R; ++m) {
+#pragma unroll
+        for (int w = P / 2; w >= 1; w /= 2) {
+            sum_D[m] += __shfl_xor_sync(0xffffffffu, sum_D[m], w * CPW);
+            sum_bias[m] += __shfl_xor_sync(0xffffffffu, sum_bias[m], w * CPW);
+            if (SPAN) sum_dt[m] += __shfl_xor_sync(0xffffffffu, sum_dt[m], w * CPW);
+        }
+        if (!live[m]) continue;
+        if (SPAN) {
+            store_state<S, PAD>(a.seg_dh + slot * hrow + hoff[m], left, dh[m]);
+            if (q == 0) a.seg_dt[static_cast<long long>(slot) * a.dim + d[m]] = sum_dt[m];
+        } else {
+            store_state<S, PAD>(a.part_a + slot * hrow + hoff[m], left, dA[m]);
+            if (a.d_state_in && found && p.tile == 0) store_state<S, PAD>(a.d_state_in + p.b * hrow + hoff[m], left, dh[m]);
+            if (q == 0) {
+                a.part_d[(2ll * slot) * a.dim + d[m]] = sum_D[m];
+                a.part_d[(2ll * slot + 1) * a.dim + d[m]] = sum_bias[m];
+            }
         }
     }
 }
 
-// The sums over the channel tiles (dB, dC of every row) and over the sequences (dA, dD, d bias), in
-// the order of the tiles and of the sequences.
+// The sums over the channel tiles (dB, dC of every row) and over the blocks' slots (dA, dD, d bias),
+// in their order.
 template <typename T>
 __global__ void __launch_bounds__(256) scan_bwd_sum_kernel(const ScanBwdArgs a, long long rows, long long n_bc,
                                                            long long n_a) {
@@ -287,23 +431,27 @@ __global__ void __launch_bounds__(256) scan_bwd_sum_kernel(const ScanBwdArgs a, 
     } else if (i < n_bc + n_a) {
         const long long e = i - n_bc;
         float s = 0.f;
-        for (int b = 0; b < a.s.n_seq; ++b) s += a.part_a[b * n_a + e];
+        for (int b = 0; b < a.n_slots; ++b) s += a.part_a[b * n_a + e];
         a.dA[e] = s;
     } else if (i < n_bc + n_a + 2 * a.dim) {
         const int e = static_cast<int>(i - n_bc - n_a);
         float s = 0.f;
-        for (int b = 0; b < a.s.n_seq; ++b) s += a.part_d[2ll * b * a.dim + e];
+        for (int b = 0; b < a.n_slots; ++b) s += a.part_d[2ll * b * a.dim + e];
         float* out = e < a.dim ? a.dD : a.dbias;
         if (out) out[e % a.dim] = s;
     }
 }
 
-template <typename T, int P, bool PAD>
+template <typename T, class Y, bool PAD, bool GATE>
 cudaError_t run(const ScanBwdArgs& a, cudaStream_t s) {
-    const unsigned grid = static_cast<unsigned>(static_cast<long long>(a.s.n_seq) * a.groups * a.tiles);
-    scan_bwd_kernel<T, P, PAD><<<grid, kWarps * 32, 0, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    const unsigned grid = static_cast<unsigned>(static_cast<long long>(a.n_slots) * a.groups * a.tiles);
+    cudaError_t e;
+    if (a.split) {
+        scan_bwd_kernel<T, Y, PAD, GATE, true><<<grid, Y::THREADS, 0, s>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    scan_bwd_kernel<T, Y, PAD, GATE, false><<<grid, Y::THREADS, 0, s>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const long long rows = a.s.cu ? a.s.L : a.s.n_seq * a.s.L;
     const long long n_bc = rows * a.groups * 2 * a.N, n_a = static_cast<long long>(a.dim) * a.N;
     const long long n = n_bc + n_a + 2 * a.dim;
@@ -311,24 +459,46 @@ cudaError_t run(const ScanBwdArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <typename T, int P>
-cudaError_t pad(const ScanBwdArgs& a, cudaStream_t s) {
-    return a.N == 4 * P ? run<T, P, false>(a, s) : run<T, P, true>(a, s);
+template <typename T, class Y>
+cudaError_t pick(const ScanBwdArgs& a, cudaStream_t s) {
+    if (a.N == Y::NP) return a.z ? run<T, Y, false, true>(a, s) : run<T, Y, false, false>(a, s);
+    return a.z ? run<T, Y, true, true>(a, s) : run<T, Y, true, false>(a, s);
 }
+
+using Lanes4 = Lanes<4, 1, 1, 2>;
+using Lanes8 = Lanes<4, 2, 2, 2>;
+using Lanes16 = Lanes<4, 4, 2, 4>;
+using Lanes32 = Lanes<4, 8, 2, 4>;
+using Lanes64 = Lanes<4, 16, 1, 4>;
+
 template <typename T>
 cudaError_t dispatch(const ScanBwdArgs& a, cudaStream_t s) {
-    if (a.N <= 4) return pad<T, 1>(a, s);
-    if (a.N <= 8) return pad<T, 2>(a, s);
-    if (a.N <= 16) return pad<T, 4>(a, s);
-    if (a.N <= 32) return pad<T, 8>(a, s);
-    return pad<T, 16>(a, s);
+    if (a.N <= 4) return pick<T, Lanes4>(a, s);
+    if (a.N <= 8) return pick<T, Lanes8>(a, s);
+    if (a.N <= 16) return pick<T, Lanes16>(a, s);
+    if (a.N <= 32) return pick<T, Lanes32>(a, s);
+    return pick<T, Lanes64>(a, s);
+}
+
+bool rows_on_16(const void* p, RowStride r, const ScanBwdArgs& a, size_t esz) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (a.s.cu || r.b * esz % 16 == 0) && r.t * esz % 16 == 0 &&
+           (a.groups == 1 || a.dim / a.groups * esz % 16 == 0);
 }
 
 }  // namespace
 
-int scan_bwd_channels(int N) { return kWarps * 32 / (N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16); }
+int scan_bwd_channels(int N) {
+    return N <= 4 ? Lanes4::CH : N <= 8 ? Lanes8::CH : N <= 16 ? Lanes16::CH : N <= 32 ? Lanes32::CH : Lanes64::CH;
+}
 
-cudaError_t launch_scan_bwd(const ScanBwdArgs& a, int dtype, cudaStream_t s) {
+cudaError_t launch_scan_bwd(const ScanBwdArgs& args, int dtype, cudaStream_t s) {
+    ScanBwdArgs a = args;
+    const size_t esz = dtype == 0 ? 4 : 2;
+    const RowStride own{a.s.L * a.dim, a.dim};
+    a.wide = (rows_on_16(a.u, a.su, a, esz) ? 1 : 0) | (rows_on_16(a.delta, a.sdt, a, esz) ? 2 : 0) |
+             (a.z && rows_on_16(a.z, a.sz, a, esz) ? 4 : 0) | (rows_on_16(a.d_out, a.sdo, a, esz) ? 8 : 0) |
+             (rows_on_16(a.du, own, a, esz) ? 16 : 0) | (rows_on_16(a.ddelta, own, a, esz) ? 32 : 0) |
+             (a.dz && rows_on_16(a.dz, own, a, esz) ? 64 : 0);
     return dtype == 0 ? dispatch<float>(a, s) : dispatch<__nv_bfloat16>(a, s);
 }
 

@@ -137,6 +137,24 @@ Split scan_split(int n_seq, long long L, long long longest, bool packed, int dim
 }
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
+
+// The same for the backward, whose blocks hold up to 64 channels: spans where whole sequences would
+// leave most of the GPU idle.
+Split bwd_split(int n_seq, long long L, bool packed, long long tiles) {
+    Split s{false, static_cast<int>((L + 16) / 16 * 16), n_seq};
+    const long long blocks = tiles * n_seq, slots = 2 * kSms, total = packed ? L : n_seq * L;
+    if (blocks * 2 > slots) return s;
+    long long spans = packed ? slots / tiles - n_seq / 2 : slots / tiles / n_seq;
+    if (spans < 1) spans = 1;
+    long long span = ((packed ? total : L) + spans - 1) / spans;
+    span = ((span < 32 ? 32 : span) + 15) / 16 * 16;
+    if (span * 2 > L) return s;
+    s.on = true;
+    s.span = static_cast<int>(span);
+    s.slots = slot_count(packed, n_seq, L, span);
+    return s;
+}
+
 }  // namespace
 
 extern "C" {
@@ -403,15 +421,34 @@ int ttt_selective_scan_step(const void* u, const void* delta, const float* A, co
     return e == cudaSuccess ? ok() : cuda_fail(e, "ttt_selective_scan_step launch");
 }
 
+namespace {
+// The backward's workspace: byte offsets of its parts.
+struct BwdLayout {
+    Split split;
+    int tiles;
+    size_t part_a, part_d, seg_dh, seg_dt, total;  // part_bc lies at 0
+};
+BwdLayout bwd_layout(int n_seq, long long L, bool packed, int dim, int groups, int N) {
+    BwdLayout y{};
+    const int ch = ttt::scan_bwd_channels(N);
+    y.tiles = (dim / groups + ch - 1) / ch;
+    y.split = bwd_split(n_seq, L, packed, static_cast<long long>(groups) * y.tiles);
+    const size_t rows = static_cast<size_t>(packed ? L : n_seq * L), state = static_cast<size_t>(dim) * N * 4;
+    const size_t slots = static_cast<size_t>(y.split.slots);
+    y.part_a = up256(y.tiles * rows * groups * 2 * N * 4);
+    y.part_d = y.part_a + up256(slots * state);
+    y.seg_dh = y.part_d + up256(slots * 2 * dim * 4);
+    y.seg_dt = y.seg_dh + (y.split.on ? up256(slots * state) : 0);
+    y.total = y.seg_dt + (y.split.on ? up256(slots * dim * 4) : 0);
+    return y;
+}
+}  // namespace
+
 long long ttt_selective_scan_backward_workspace_bytes(int n_seq, long long L, int packed, int dim, int groups, int d_state) {
     const int rc = check_scan(n_seq, L, dim, groups, d_state, TTT_F32, 0);
     if (rc) return rc;
     ok();
-    const int ch = ttt::scan_bwd_channels(d_state), tiles = (dim / groups + ch - 1) / ch;
-    const size_t rows = static_cast<size_t>(packed ? L : n_seq * L);
-    return static_cast<long long>(up256(tiles * rows * groups * 2 * d_state * 4) +
-                                  up256(static_cast<size_t>(n_seq) * dim * d_state * 4) +
-                                  up256(static_cast<size_t>(n_seq) * 2 * dim * 4));
+    return static_cast<long long>(bwd_layout(n_seq, L, packed != 0, dim, groups, d_state).total);
 }
 
 int ttt_selective_scan_backward(const void* u, const void* delta, const float* A, const void* B, const void* C,
@@ -475,13 +512,14 @@ int ttt_selective_scan_backward(const void* u, const void* delta, const float* A
     a.ckpt = ckpt; a.d_state_out = d_state_out;
     a.du = du; a.ddelta = d_delta; a.dB = dB; a.dC = dC; a.dz = dz; a.dA = dA; a.dD = dD; a.dbias = d_delta_bias;
     a.d_state_in = d_state_in;
-    const int ch = ttt::scan_bwd_channels(d_state);
-    a.tiles = (dim / groups + ch - 1) / ch;
+    const BwdLayout y = bwd_layout(n_seq, L, packed, dim, groups, d_state);
     char* w = static_cast<char*>(workspace);
+    a.tiles = y.tiles; a.span = y.split.span; a.n_slots = static_cast<int>(y.split.slots); a.split = y.split.on;
     a.part_bc = reinterpret_cast<float*>(w);
-    w += up256(static_cast<size_t>(a.tiles) * rows * bc * 2 * 4);
-    a.part_a = reinterpret_cast<float*>(w);
-    a.part_d = reinterpret_cast<float*>(w + up256(n_seq * state));
+    a.part_a = reinterpret_cast<float*>(w + y.part_a);
+    a.part_d = reinterpret_cast<float*>(w + y.part_d);
+    a.seg_dh = reinterpret_cast<float*>(w + y.seg_dh);
+    a.seg_dt = reinterpret_cast<float*>(w + y.seg_dt);
     const cudaError_t e = ttt::launch_scan_bwd(a, dtype, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ok() : cuda_fail(e, "ttt_selective_scan_backward launch");
 }

@@ -103,9 +103,13 @@ struct ScanBwdArgs {
     float *dA, *dD, *dbias;
     float* d_state_in;           // [n_seq][dim][N] or nullptr
     int tiles;                   // channel tiles per group
+    int span, n_slots, split;    // as in ScanArgs, span a multiple of kScanChunk
     float* part_bc;              // [tiles][rows][groups][2][N]
-    float* part_a;               // [n_seq][dim][N]
-    float* part_d;               // [n_seq][2][dim]: d D, d bias
+    float* part_a;               // [n_slots][dim][N]
+    float* part_d;               // [n_slots][2][dim]: d D, d bias
+    float* seg_dh;               // [n_slots][dim][N]: what each span passes back, from nothing behind it
+    float* seg_dt;               // [n_slots][dim]: each span's sum of dt
+    int wide;                    // bits: the rows of u, delta, z, d_out, du, d delta, dz start on 16-byte boundaries
 };
 
 constexpr int kCacheMaxTensors = 64;
