@@ -105,6 +105,9 @@ __device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&v)[VEC]
         const uint2 t = *reinterpret_cast<const uint2*>(p);
         const float2 f = unpack_bf16x2(t.x), g = unpack_bf16x2(t.y);
         v[0] = f.x; v[1] = f.y; v[2] = g.x; v[3] = g.y;
+    } else if constexpr (VEC == 2) {
+        const float2 f = unpack_bf16x2(*reinterpret_cast<const uint32_t*>(p));
+        v[0] = f.x; v[1] = f.y;
     } else {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[i] = __bfloat162float(p[i]);
@@ -128,6 +131,8 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&v)[VEC
                                                   pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
     } else if constexpr (VEC == 4) {
         *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    } else if constexpr (VEC == 2) {
+        *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v[0], v[1]);
     } else {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) p[i] = __float2bfloat16_rn(v[i]);
