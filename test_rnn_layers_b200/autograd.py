@@ -1,4 +1,5 @@
-"""torch.autograd face of the TTT-Linear scan, for training through it.
+"""torch.autograd face of the TTT-Linear scan, of the causal convolution and of the selective scan, for
+training through them.
 
 `ttt_linear(XQ, XK, XV, lr, W0, b0, ln_w, ln_b, ...)` returns (out, W_last, b_last) like
 `ttt_linear_forward`, recording the call so that `.backward()` reaches XQ, XK, XV, lr, W0, b0, ln_w
@@ -8,12 +9,19 @@ start of every checkpoint group (ttt_linear_forward_ckpt) and the backward rebui
 from it (ttt_linear_backward_ckpt), instead of running the state recursion a second time.  Both
 directions run in libttt.so's kernels; this module only passes tensors between autograd and the
 C ABI.  token_eta, eps and the mini-batch size are constants.
+
+`causal_conv` and `selective_scan` do the same for ttt_causal_conv_forward / _backward and
+ttt_selective_scan_forward / _backward (whose forward keeps the state before every 8th token).
 """
 from __future__ import annotations
 
 import torch
 
-from . import _act_sizes, ttt_linear_backward, ttt_linear_ckpt_bytes, ttt_linear_forward
+from torch.autograd.function import once_differentiable
+
+from . import (_act_sizes, _seq_sizes, ttt_causal_conv_backward, ttt_causal_conv_forward, ttt_linear_backward,
+               ttt_linear_ckpt_bytes, ttt_linear_forward, ttt_selective_scan_backward, ttt_selective_scan_ckpt_bytes,
+               ttt_selective_scan_forward)
 
 
 class _TTTLinear(torch.autograd.Function):
@@ -49,3 +57,65 @@ def ttt_linear(XQ, XK, XV, lr, W0, b0, ln_w, ln_b, mini_batch: int = 16, eps: fl
     token_major), with gradients for every input (see ttt_linear_forward and ttt_linear_backward
     in include/ttt.h)."""
     return _TTTLinear.apply(XQ, XK, XV, lr, W0, b0, ln_w, ln_b, mini_batch, eps, token_eta, ckpt_group, token_major)
+
+
+def _rows(t):
+    """An upstream gradient with contiguous channels (its rows may be strided or repeated)."""
+    return t if t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
+
+
+class _CausalConv(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, silu, cu_seqlens):
+        ctx.save_for_backward(x, weight, bias, cu_seqlens)
+        ctx.silu = silu
+        return ttt_causal_conv_forward(x, weight, bias, silu=silu, cu_seqlens=cu_seqlens)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_out):
+        x, weight, bias, cu_seqlens = ctx.saved_tensors
+        g = ttt_causal_conv_backward(x, weight, _rows(d_out), bias, silu=ctx.silu, cu_seqlens=cu_seqlens)
+        return g["dx"], g["dweight"], g["dbias"], None, None
+
+
+def causal_conv(x, weight, bias=None, silu: bool = True, cu_seqlens=None):
+    """ttt_causal_conv_forward of whole sequences (starting from zeros), with gradients for x, weight and
+    bias: x [n_seq, L, dim], or packed rows [L, dim] with cu_seqlens."""
+    return _CausalConv.apply(x, weight, bias, silu, cu_seqlens)
+
+
+class _SelectiveScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, u, delta, A, B, C, D, z, delta_bias, state_in, softplus, cu_seqlens, max_seqlen, want_state):
+        n_seq, L, _ = _seq_sizes(u, "u", cu_seqlens)
+        dim, N = A.shape
+        packed = cu_seqlens is not None
+        ckpt = torch.empty(ttt_selective_scan_ckpt_bytes(n_seq, L, dim, N, packed) // 4, device=u.device)
+        state = torch.empty((n_seq, dim, N), device=u.device) if want_state else None
+        out = ttt_selective_scan_forward(u, delta, A, B, C, D=D, z=z, delta_bias=delta_bias, softplus=softplus,
+                                         state_in=state_in, state_out=state, cu_seqlens=cu_seqlens,
+                                         max_seqlen=max_seqlen, ckpt=ckpt)
+        ctx.save_for_backward(u, delta, A, B, C, D, z, delta_bias, cu_seqlens, ckpt)
+        ctx.cfg = (softplus, state_in is not None)
+        return (out, state) if want_state else out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_out, d_state=None):
+        u, delta, A, B, C, D, z, delta_bias, cu_seqlens, ckpt = ctx.saved_tensors
+        softplus, has_state = ctx.cfg
+        g = ttt_selective_scan_backward(u, delta, A, B, C, _rows(d_out), ckpt, D=D, z=z, delta_bias=delta_bias,
+                                        softplus=softplus, d_state_out=None if d_state is None else d_state.contiguous(),
+                                        state_in_grad=has_state, cu_seqlens=cu_seqlens)
+        return (g["du"], g["ddelta"], g["dA"], g["dB"], g["dC"], g["dD"], g["dz"], g["ddelta_bias"], g["dstate_in"],
+                None, None, None, None)
+
+
+def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus: bool = True, state_in=None,
+                   cu_seqlens=None, max_seqlen: int = 0, return_state: bool = False):
+    """ttt_selective_scan_forward with gradients for every input: u, delta, z [n_seq, L, dim] and B, C [n_seq, L,
+    groups, d_state], or packed rows with cu_seqlens; state_in [n_seq, dim, d_state] or None (zeros).
+    Returns out, or (out, states after the sequences [n_seq, dim, d_state]) with return_state."""
+    return _SelectiveScan.apply(u, delta, A, B, C, D, z, delta_bias, state_in, softplus, cu_seqlens, max_seqlen,
+                                return_state)
