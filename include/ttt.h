@@ -665,10 +665,11 @@ int ttt_selective_scan_backward(const void* u, const void* delta, const float* A
                                 long long workspace_bytes, void* stream);
 
 /* ---- pages of a cache of recurrent states ------------------------------------------------------
- * A cache is up to 64 tensors (HOST arrays of device pointers and of bytes per page), each [n_pages,
+ * A cache is up to 512 tensors (HOST arrays of device pointers and of bytes per page), each [n_pages,
  * ...] contiguous with one page a sequence: the decode caches of ttt_linear_decode_step and
  * ttt_linear_decode_step_hist (W, b, W_grad or hist, b_grad), the states of ttt_causal_conv_step and
- * ttt_selective_scan_step, of one layer or of several.  Two int32 arrays on the device keep the books:
+ * ttt_selective_scan_step, of one layer or of all of them: the books change with the call, so one call takes
+ * every tensor they stand for (more than 512: ttt_cache_copy with the pages that the call returned).  Two int32 arrays on the device keep the books:
  *   table [n_rows]   the page of each sequence row, or negative;
  *   owner [n_pages]  the sequence row of each page, or negative (free).
  * They start out as -1 throughout and are changed by these calls only.  Everything is decided on the

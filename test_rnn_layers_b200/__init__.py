@@ -10,6 +10,8 @@ If libttt.so is missing this module raises on first use: there is no CPU fallbac
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 
 import torch
@@ -599,109 +601,125 @@ def ttt_linear_backward(XQ, XK, XV, lr, W0, b0, ln_w, ln_b, d_out, dW_last=None,
 
 # ---- causal convolution, selective scan, cache pages -------------------------------------------------
 
-class _On:
-    """The device and stream of a call: its tensors' device is made current, and what the call
-    allocates belongs to the stream it runs on.  (Decode steps are a few microseconds of GPU work, so
-    the checks below are written to cost the host little.)"""
+# A decode step is a few microseconds of GPU work, so what follows is written to cost the host little: an
+# argument that is as it should be passes one chain of comparisons, and only one that is not is looked
+# at closely.
 
-    __slots__ = ("index", "device", "handle", "_ctx")
+def _here(t, stream):
+    """(device index, stream handle, context to run in or None): the tensors' device is made current, and
+    what a call allocates belongs to the stream it runs on."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("the first argument must be a torch.Tensor")
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("the tensors must be CUDA tensors (there is no CPU path)")
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+        return index, handle, None if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    return index, stream.cuda_stream, torch.cuda.stream(stream)
 
-    def __init__(self, t, stream):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("the first argument must be a torch.Tensor")
-        self.index = t.get_device()
-        if self.index < 0:
-            raise ValueError("the tensors must be CUDA tensors (there is no CPU path)")
-        self.device = t.device
-        if stream is None:
-            self.handle = torch._C._cuda_getCurrentRawStream(self.index)
-            self._ctx = None if torch._C._cuda_getDevice() == self.index else torch.cuda.device(self.index)
-        else:
-            if stream.device != self.device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
-            self.handle = stream.cuda_stream
-            self._ctx = torch.cuda.stream(stream)
 
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return self
+def _in_context(fn):
+    """Run fn(index, handle, first, ...) on the device of its first tensor and on the stream given."""
+    sig = inspect.signature(fn)
+    ps = list(sig.parameters.values())[2:]
+    name = ps[0].name
 
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            return self._ctx.__exit__(*exc)
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        index, handle, ctx = _here(args[0] if args else kw.get(name), stream)
+        if ctx is None:
+            return fn(index, handle, *args, **kw)
+        with ctx:
+            return fn(index, handle, *args, **kw)
+    call.__signature__ = sig.replace(parameters=ps + [inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
+    return call
 
-    def ptr(self, t, name, dtype=None, shape=None):
-        """Address of a contiguous tensor (None: no tensor)."""
-        if t is None:
-            return None
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.get_device() != self.index:
-            raise ValueError(f"{name} is on {t.device}, the first argument on {self.device}")
-        if dtype is not None and t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if shape is not None and t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+
+def _refuse(t, name, index, dtype, shape):
+    """Say what is wrong with a tensor (its strides, if nothing else is)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the first argument on cuda:{index}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _need_ptr(t, name, index, dtype, shape):
+    """Address of a contiguous tensor of this type and shape."""
+    if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
-
-    def need(self, t, name, dtype=None, shape=None):
-        if t is None:
-            raise TypeError(f"{name} must be a torch.Tensor")
-        return self.ptr(t, name, dtype, shape)
-
-    def workspace(self, nbytes: int, given=None):
-        if given is not None:
-            self.need(given, "workspace", torch.uint8)
-            return given
-        return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+    _refuse(t, name, index, dtype, shape)
 
 
-class _Rows:
-    """The operands of a call that are rows of channels: their addresses, and their (batch, token) element
-    strides unless all of them are contiguous."""
+def _maybe_ptr(t, name, index, dtype, shape):
+    return None if t is None else _need_ptr(t, name, index, dtype, shape)
 
-    __slots__ = ("on", "dtype", "views")
 
-    def __init__(self, on, dtype):
-        self.on, self.dtype, self.views = on, dtype, []
+def _cu_ptr(t, index):
+    if t is None:
+        return None
+    return _need_ptr(t, "cu_seqlens", index, torch.int32, t.shape if isinstance(t, torch.Tensor) else None)
 
-    def __call__(self, t, name, shape, inner: int = 1):
-        """The address of t (None: no tensor); its last `inner` dimensions must be contiguous."""
-        if t is None:
-            self.views.append(None)
-            return None
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.get_device() != self.on.index:
-            raise ValueError(f"{name} is on {t.device}, the first argument on {self.on.device}")
-        if t.dtype != self.dtype:
-            raise TypeError(f"{name} must be {self.dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if t.is_contiguous():
-            self.views.append(None)
-        else:
+
+def _row_ptr(t, name, index, dtype, shape, views, at, inner=1):
+    """Address of an operand that is rows of channels (its last `inner` dimensions contiguous); one that is
+    not contiguous leaves its place among the operands and its row strides in `views`."""
+    if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape:
+        if not t.is_contiguous():
             want = 1
             for k in range(1, inner + 1):
                 if t.shape[-k] > 1 and t.stride(-k) != want:
                     raise ValueError(f"{name}: its channels must be contiguous, got strides {tuple(t.stride())}")
                 want *= t.shape[-k]
-            self.views.append(t.stride()[:-inner])
+            views.append((at, t.stride()[:-inner]))
         return t.data_ptr()
+    _refuse(t, name, index, dtype, shape)
 
-    def strides(self, *contiguous):
-        """The ABI's strides: None if every operand is contiguous, else (batch, token) of each (`contiguous`
-        holds what those are for the operands that are)."""
-        if not any(v is not None for v in self.views):
-            return None
-        flat = []
-        for v, c in zip(self.views, contiguous):
-            v = c if v is None else v
-            flat += [0] * (len(c) - len(v)) + [int(x) for x in v]
-        return (ctypes.c_longlong * len(flat))(*flat)
+
+def _strides(views, *contiguous):
+    """The ABI's strides, (batch, token) of each operand: None if all of them are contiguous."""
+    if not views:
+        return None
+    flat = [int(x) for c in contiguous for x in c]
+    per = len(contiguous[0])
+    for at, v in views:
+        flat[per * at + per - len(v):per * at + per] = [int(x) for x in v]
+        if len(v) < per:
+            flat[per * at] = 0
+    return (ctypes.c_longlong * len(flat))(*flat)
+
+
+def _space(nbytes, given, index):
+    """A call's workspace: the one given, or a new one on the stream of the call."""
+    if given is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{index}")
+    _need_ptr(given, "workspace", index, torch.uint8, given.shape if isinstance(given, torch.Tensor) else None)
+    return given
+
+
+def _f32(shape, like):
+    return torch.empty(shape, dtype=torch.float32, device=like.device)
+
+
+def _out_like(x):
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
+_CODES = {torch.float32: TTT_F32, torch.bfloat16: TTT_BF16}
+
+
+def _code(x) -> int:
+    c = _CODES.get(x.dtype)
+    if c is None:
+        raise TypeError(f"activations must be float32 or bfloat16, got {x.dtype}")
+    return c
 
 
 def _bytes(n) -> int:
@@ -723,60 +741,65 @@ def _seq_sizes(x, name, cu_seqlens):
     return cu_seqlens.numel() - 1, x.shape[0], (x.shape[0],)
 
 
-def _pool(on, pages, n_seq, *pools):
+def _pool(index, pages, n_seq, one, two=None):
     """(address of pages, n_pages) for the state pools given (each None or [n_pages, ...])."""
-    sizes = {p.shape[0] for p in pools if p is not None}
-    if len(sizes) > 1:
+    if one is None:
+        one, two = two, None
+    n = 0 if one is None else one.shape[0]
+    if two is not None and two.shape[0] != n:
         raise ValueError("state_in and state_out must have the same number of pages")
-    return on.ptr(pages, "pages", torch.int32, (n_seq,)), sizes.pop() if sizes else 0
+    return None if pages is None else _need_ptr(pages, "pages", index, torch.int32, (n_seq,)), n
 
 
-def ttt_causal_conv_forward(x, weight, bias=None, silu: bool = True, state_in=None, state_out=None, pages=None,
-                            cu_seqlens=None, out=None, stream=None):
+@_in_context
+def ttt_causal_conv_forward(index, handle, x, weight, bias=None, silu: bool = True, state_in=None, state_out=None,
+                            pages=None, cu_seqlens=None, out=None):
     """Short causal convolution over tokens (one filter of 2 to 4 taps a channel, then silu): x [n_seq, L,
     dim], or packed rows [L, dim] with cu_seqlens (int32 [n_seq + 1]); weight [dim, width], bias [dim]
     float32.  state_in / state_out: pools [n_pages, width - 1, dim] in x's dtype holding the inputs
     before / after each sequence, in the pages named by `pages` (int32 [n_seq], default page b).
     x may be a strided view with contiguous channels.  Rows of a given `out` outside every sequence stay as
     they were; in one allocated here they are zero.  Returns out (see include/ttt.h)."""
-    with _On(x, stream) as on:
-        n_seq, L, lead = _seq_sizes(x, "x", cu_seqlens)
-        dim, width, dt = x.shape[-1], weight.shape[-1], x.dtype
-        flags = TTT_FLAG_SILU if silu else 0
-        if out is None:
-            out = torch.empty(x.shape, dtype=dt, device=on.device)
-            flags |= TTT_FLAG_ZERO_REST
-        rows = _Rows(on, dt)
-        px, po = rows(x, "x", x.shape), rows(out, "out", x.shape)
-        pp, n_pages = _pool(on, pages, n_seq, state_in, state_out)
-        st = (n_pages, width - 1, dim)
-        c = (L * dim, dim)
-        _check(lib().ttt_causal_conv_forward(px, on.need(weight, "weight", torch.float32, (dim, width)),
-                                             on.ptr(bias, "bias", torch.float32, (dim,)), rows.strides(c, c),
-                                             on.ptr(cu_seqlens, "cu_seqlens", torch.int32),
-                                             on.ptr(state_in, "state_in", dt, st), on.ptr(state_out, "state_out", dt, st),
-                                             pp, n_pages, n_seq, L, dim, width, _dtype_code(x), flags, po, on.handle))
-        return out
+    code = _code(x)
+    n_seq, L, _ = _seq_sizes(x, "x", cu_seqlens)
+    dim, width, dt, views = x.shape[-1], weight.shape[-1], x.dtype, []
+    flags = TTT_FLAG_SILU if silu else 0
+    px = _row_ptr(x, "x", index, dt, x.shape, views, 0)
+    pw = _need_ptr(weight, "weight", index, torch.float32, (dim, width))
+    pb = _maybe_ptr(bias, "bias", index, torch.float32, (dim,))
+    pp, n_pages = _pool(index, pages, n_seq, state_in, state_out)
+    st = (n_pages, width - 1, dim)
+    pi, po = _maybe_ptr(state_in, "state_in", index, dt, st), _maybe_ptr(state_out, "state_out", index, dt, st)
+    pc = _cu_ptr(cu_seqlens, index)
+    if out is None:
+        out = _out_like(x)
+        flags |= TTT_FLAG_ZERO_REST
+    py, c = _row_ptr(out, "out", index, dt, x.shape, views, 1), (L * dim, dim)
+    _check(lib().ttt_causal_conv_forward(px, pw, pb, _strides(views, c, c), pc, pi, po, pp, n_pages, n_seq, L, dim, width,
+                                         code, flags, py, handle))
+    return out
 
 
-def ttt_causal_conv_step(x, state, weight, bias=None, silu: bool = True, pages=None, out=None, stream=None):
+@_in_context
+def ttt_causal_conv_step(index, handle, x, state, weight, bias=None, silu: bool = True, pages=None, out=None):
     """One token of each sequence through the convolution: x [n_seq, dim]; `state` (a pool [n_pages, width
     - 1, dim]) moves on by one row in place.  Rows whose page is negative give zeros.  Returns out."""
-    with _On(x, stream) as on:
-        if x.dim() != 2:
-            raise ValueError(f"x must be [n_seq, dim], got {tuple(x.shape)}")
-        n_seq, dim = x.shape
-        width, dt = weight.shape[-1], x.dtype
-        if out is None:
-            out = torch.empty((n_seq, dim), dtype=dt, device=on.device)
-        rows = _Rows(on, dt)
-        px, po = rows(x, "x", x.shape), rows(out, "out", x.shape)
-        pp, n_pages = _pool(on, pages, n_seq, state)
-        _check(lib().ttt_causal_conv_step(px, on.need(weight, "weight", torch.float32, (dim, width)),
-                                          on.ptr(bias, "bias", torch.float32, (dim,)), rows.strides((dim,), (dim,)),
-                                          on.need(state, "state", dt, (n_pages, width - 1, dim)), pp, n_pages, n_seq,
-                                          dim, width, _dtype_code(x), TTT_FLAG_SILU if silu else 0, po, on.handle))
-        return out
+    code = _code(x)
+    if x.dim() != 2:
+        raise ValueError(f"x must be [n_seq, dim], got {tuple(x.shape)}")
+    n_seq, dim = x.shape
+    width, dt, views = weight.shape[-1], x.dtype, []
+    px = _row_ptr(x, "x", index, dt, x.shape, views, 0)
+    pw = _need_ptr(weight, "weight", index, torch.float32, (dim, width))
+    pb = _maybe_ptr(bias, "bias", index, torch.float32, (dim,))
+    pp, n_pages = _pool(index, pages, n_seq, state)
+    ps = _need_ptr(state, "state", index, dt, (n_pages, width - 1, dim))
+    if out is None:
+        out = _out_like(x)
+    py = _row_ptr(out, "out", index, dt, x.shape, views, 1)
+    _check(lib().ttt_causal_conv_step(px, pw, pb, _strides(views, (dim,), (dim,)), ps, pp, n_pages, n_seq, dim, width, code,
+                                      TTT_FLAG_SILU if silu else 0, py, handle))
+    return out
 
 
 def ttt_causal_conv_backward_workspace_bytes(n_seq: int, L: int, dim: int, width: int, packed: bool = False,
@@ -786,35 +809,31 @@ def ttt_causal_conv_backward_workspace_bytes(n_seq: int, L: int, dim: int, width
                                                                  TTT_F32 if dtype == torch.float32 else TTT_BF16))
 
 
-def ttt_causal_conv_backward(x, weight, d_out, bias=None, silu: bool = True, state_in=None, d_state_out=None,
-                             cu_seqlens=None, workspace=None, stream=None):
+@_in_context
+def ttt_causal_conv_backward(index, handle, x, weight, d_out, bias=None, silu: bool = True, state_in=None,
+                             d_state_out=None, cu_seqlens=None, workspace=None):
     """Gradients of ttt_causal_conv_forward for d_out (and d_state_out, the gradient of the states after
     each sequence; state_in and d_state_out are [n_seq, width - 1, dim] here, sequence b at b).  Returns a
     dict: dx (x's dtype; zero in rows outside every sequence), dweight [dim, width], dbias [dim] float32
     (None without bias), dstate_in (None without state_in)."""
-    with _On(x, stream) as on:
-        n_seq, L, lead = _seq_sizes(x, "x", cu_seqlens)
-        dim, width, dt = x.shape[-1], weight.shape[-1], x.dtype
-        rows = _Rows(on, dt)
-        px, pd = rows(x, "x", x.shape), rows(d_out, "d_out", x.shape)
-        if pd is None:
-            raise TypeError("d_out must be a torch.Tensor")
-        st, c = (n_seq, width - 1, dim), (L * dim, dim)
-        pw = on.need(weight, "weight", torch.float32, (dim, width))
-        ws = on.workspace(ttt_causal_conv_backward_workspace_bytes(n_seq, L, dim, width, cu_seqlens is not None, dt),
-                          workspace)
-        g = {"dx": torch.empty(x.shape, dtype=dt, device=on.device),
-             "dweight": torch.empty((dim, width), device=on.device),
-             "dbias": None if bias is None else torch.empty(dim, device=on.device),
-             "dstate_in": None if state_in is None else torch.empty_like(state_in)}
-        _check(lib().ttt_causal_conv_backward(px, pw, on.ptr(bias, "bias", torch.float32, (dim,)), rows.strides(c, c),
-                                              on.ptr(cu_seqlens, "cu_seqlens", torch.int32),
-                                              on.ptr(state_in, "state_in", dt, st), n_seq, L, dim, width,
-                                              _dtype_code(x), (TTT_FLAG_SILU if silu else 0) | TTT_FLAG_ZERO_REST, pd,
-                                              on.ptr(d_state_out, "d_state_out", dt, st), g["dx"].data_ptr(),
-                                              g["dweight"].data_ptr(), _addr(g["dbias"]), _addr(g["dstate_in"]),
-                                              ws.data_ptr(), ws.numel(), on.handle))
-        return g
+    code = _code(x)
+    n_seq, L, _ = _seq_sizes(x, "x", cu_seqlens)
+    dim, width, dt, views = x.shape[-1], weight.shape[-1], x.dtype, []
+    px = _row_ptr(x, "x", index, dt, x.shape, views, 0)
+    pd = _row_ptr(d_out, "d_out", index, dt, x.shape, views, 1)
+    pw = _need_ptr(weight, "weight", index, torch.float32, (dim, width))
+    pb = _maybe_ptr(bias, "bias", index, torch.float32, (dim,))
+    st, c = (n_seq, width - 1, dim), (L * dim, dim)
+    pi, ps = _maybe_ptr(state_in, "state_in", index, dt, st), _maybe_ptr(d_state_out, "d_state_out", index, dt, st)
+    pc = _cu_ptr(cu_seqlens, index)
+    ws = _space(ttt_causal_conv_backward_workspace_bytes(n_seq, L, dim, width, cu_seqlens is not None, dt), workspace, index)
+    g = {"dx": _out_like(x), "dweight": _f32((dim, width), x), "dbias": None if bias is None else _f32((dim,), x),
+         "dstate_in": None if state_in is None else torch.empty_like(state_in)}
+    _check(lib().ttt_causal_conv_backward(px, pw, pb, _strides(views, c, c), pc, pi, n_seq, L, dim, width, code,
+                                          (TTT_FLAG_SILU if silu else 0) | TTT_FLAG_ZERO_REST, pd, ps, g["dx"].data_ptr(),
+                                          g["dweight"].data_ptr(), _addr(g["dbias"]), _addr(g["dstate_in"]),
+                                          ws.data_ptr(), ws.numel(), handle))
+    return g
 
 
 def _addr(t):
@@ -838,43 +857,39 @@ def ttt_selective_scan_backward_workspace_bytes(n_seq: int, L: int, dim: int, d_
     return _bytes(lib().ttt_selective_scan_backward_workspace_bytes(n_seq, L, int(packed), dim, groups, d_state))
 
 
-def _scan_operands(on, rows, u, delta, A, B, C, D, z, delta_bias, lead):
-    """Check the scan's inputs (rows of shape `lead`): (dim, groups, d_state), the addresses in the ABI's
-    order, and the strides of contiguous operands."""
-    dim, N = u.shape[-1], A.shape[-1]
+def _scan_operands(index, u, delta, A, B, C, D, z, delta_bias, lead, views):
+    """Check the scan's inputs (rows of shape `lead`): (dim, groups, d_state), and the addresses in the ABI's
+    order."""
+    dim, N, dt = u.shape[-1], A.shape[-1], u.dtype
     if B.dim() != len(lead) + 2:
         raise ValueError(f"B must be {(*lead, 'groups', 'd_state')}, got {tuple(B.shape)}")
     G = B.shape[-2]
-    for t, name in ((delta, "delta"), (C, "C")):
-        if t is None:
-            raise TypeError(f"{name} must be a torch.Tensor")
-    wide, narrow = (*lead, dim), (*lead, G, N)
-    pu, pd = rows(u, "u", wide), rows(delta, "delta", wide)
-    pB, pC, pz = rows(B, "B", narrow, 2), rows(C, "C", narrow, 2), rows(z, "z", wide)
-    ptrs = (pu, pd, on.need(A, "A", torch.float32, (dim, N)), pB, pC, on.ptr(D, "D", torch.float32, (dim,)), pz,
-            on.ptr(delta_bias, "delta_bias", torch.float32, (dim,)))
-    if len(lead) == 1:
-        w, n = (dim,), (G * N,)
-    else:
-        w, n = (lead[1] * dim, dim), (lead[1] * G * N, G * N)
-    return dim, G, N, ptrs, (w, w, n, n, w, w)
+    wide, narrow = u.shape, (*lead, G, N)
+    return dim, G, N, (_row_ptr(u, "u", index, dt, wide, views, 0), _row_ptr(delta, "delta", index, dt, wide, views, 1),
+                       _need_ptr(A, "A", index, torch.float32, (dim, N)), _row_ptr(B, "B", index, dt, narrow, views, 2, 2),
+                       _row_ptr(C, "C", index, dt, narrow, views, 3, 2), _maybe_ptr(D, "D", index, torch.float32, (dim,)),
+                       None if z is None else _row_ptr(z, "z", index, dt, wide, views, 4),
+                       _maybe_ptr(delta_bias, "delta_bias", index, torch.float32, (dim,)))
 
 
-def _packed_strides(contiguous):
-    """Strides of packed rows: the token stride alone stands for (0, token)."""
-    return tuple((0, *c) for c in contiguous)
+def _scan_strides(views, L, dim, G, N):
+    if not views:
+        return None
+    w, n = (L * dim, dim), (L * G * N, G * N)
+    return _strides(views, w, w, n, n, w, w)
 
 
-def _check_ckpt(on, ckpt, n_seq, L, dim, N, packed):
-    p = on.need(ckpt, "ckpt", torch.float32)
+def _ckpt_ptr(ckpt, index, n_seq, L, dim, N, packed):
+    p = _need_ptr(ckpt, "ckpt", index, torch.float32, ckpt.shape if isinstance(ckpt, torch.Tensor) else None)
     if ckpt.numel() * 4 < ttt_selective_scan_ckpt_bytes(n_seq, L, dim, N, packed):
         raise ValueError("ckpt is smaller than ttt_selective_scan_ckpt_bytes(...)")
     return p
 
 
-def ttt_selective_scan_forward(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus: bool = True,
+@_in_context
+def ttt_selective_scan_forward(index, handle, u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus: bool = True,
                                state_in=None, state_out=None, pages=None, cu_seqlens=None, max_seqlen: int = 0,
-                               ckpt=None, out=None, workspace=None, stream=None):
+                               ckpt=None, out=None, workspace=None):
     """Selective state space scan: u, delta, z [n_seq, L, dim] and B, C [n_seq, L, groups, d_state], or packed
     rows ([L, dim], [L, groups, d_state]) with cu_seqlens; A [dim, d_state], D, delta_bias [dim] float32.
     state_in / state_out: float32 pools [n_pages, dim, d_state], in the pages named by `pages` (int32
@@ -883,115 +898,127 @@ def ttt_selective_scan_forward(u, delta, A, B, C, D=None, z=None, delta_bias=Non
     ttt_selective_scan_backward needs.  Activations may be strided views with contiguous channels.  Rows of
     a given `out` outside every sequence stay as they were; in one allocated here they are zero.
     Returns out (see include/ttt.h)."""
-    with _On(u, stream) as on:
-        n_seq, L, lead = _seq_sizes(u, "u", cu_seqlens)
-        packed = cu_seqlens is not None
-        flags = TTT_FLAG_SOFTPLUS if softplus else 0
-        if out is None:
-            out = torch.empty(u.shape, dtype=u.dtype, device=on.device)
-            flags |= TTT_FLAG_ZERO_REST
-        rows = _Rows(on, u.dtype)
-        dim, G, N, ptrs, c = _scan_operands(on, rows, u, delta, A, B, C, D, z, delta_bias, lead)
-        po = rows(out, "out", u.shape)
-        pp, n_pages = _pool(on, pages, n_seq, state_in, state_out)
-        st = (n_pages, dim, N)
-        pc = None if ckpt is None else _check_ckpt(on, ckpt, n_seq, L, dim, N, packed)
-        need = ttt_selective_scan_workspace_bytes(n_seq, L, dim, N, G, packed, max_seqlen)
-        ws = on.workspace(need, workspace) if need or workspace is not None else None
-        _check(lib().ttt_selective_scan_forward(*ptrs, rows.strides(*(_packed_strides(c) if packed else c)),
-                                                on.ptr(cu_seqlens, "cu_seqlens", torch.int32), max_seqlen,
-                                                on.ptr(state_in, "state_in", torch.float32, st),
-                                                on.ptr(state_out, "state_out", torch.float32, st), pp, n_pages, n_seq, L,
-                                                dim, G, N, _dtype_code(u), flags, po, pc, _addr(ws),
-                                                0 if ws is None else ws.numel(), on.handle))
-        return out
+    code = _code(u)
+    n_seq, L, lead = _seq_sizes(u, "u", cu_seqlens)
+    packed, views = cu_seqlens is not None, []
+    dim, G, N, ptrs = _scan_operands(index, u, delta, A, B, C, D, z, delta_bias, lead, views)
+    flags = TTT_FLAG_SOFTPLUS if softplus else 0
+    pp, n_pages = _pool(index, pages, n_seq, state_in, state_out)
+    st = (n_pages, dim, N)
+    pi = _maybe_ptr(state_in, "state_in", index, torch.float32, st)
+    po = _maybe_ptr(state_out, "state_out", index, torch.float32, st)
+    pk = None if ckpt is None else _ckpt_ptr(ckpt, index, n_seq, L, dim, N, packed)
+    pc = _cu_ptr(cu_seqlens, index)
+    need = ttt_selective_scan_workspace_bytes(n_seq, L, dim, N, G, packed, max_seqlen)
+    ws = _space(need, workspace, index) if need or workspace is not None else None
+    if out is None:
+        out = _out_like(u)
+        flags |= TTT_FLAG_ZERO_REST
+    py = _row_ptr(out, "out", index, u.dtype, u.shape, views, 5)
+    _check(lib().ttt_selective_scan_forward(*ptrs, _scan_strides(views, L, dim, G, N), pc, max_seqlen, pi, po, pp, n_pages,
+                                            n_seq, L, dim, G, N, code, flags, py, pk, _addr(ws),
+                                            0 if ws is None else ws.numel(), handle))
+    return out
 
 
-def ttt_selective_scan_step(u, delta, A, B, C, state, D=None, z=None, delta_bias=None, softplus: bool = True,
-                            pages=None, out=None, stream=None):
+@_in_context
+def ttt_selective_scan_step(index, handle, u, delta, A, B, C, state, D=None, z=None, delta_bias=None,
+                            softplus: bool = True, pages=None, out=None):
     """One token of each sequence through the scan: u, delta, z [n_seq, dim], B, C [n_seq, groups, d_state];
     `state` (a float32 pool [n_pages, dim, d_state]) is updated in place.  Rows whose page is negative
     give zeros.  Returns out."""
-    with _On(u, stream) as on:
-        if u.dim() != 2:
-            raise ValueError(f"u must be [n_seq, dim], got {tuple(u.shape)}")
-        n_seq = u.shape[0]
-        if out is None:
-            out = torch.empty(u.shape, dtype=u.dtype, device=on.device)
-        rows = _Rows(on, u.dtype)
-        dim, G, N, ptrs, c = _scan_operands(on, rows, u, delta, A, B, C, D, z, delta_bias, (n_seq,))
-        po = rows(out, "out", u.shape)
-        pp, n_pages = _pool(on, pages, n_seq, state)
-        _check(lib().ttt_selective_scan_step(*ptrs, rows.strides(*c),
-                                             on.need(state, "state", torch.float32, (n_pages, dim, N)), pp, n_pages, n_seq,
-                                             dim, G, N, _dtype_code(u), TTT_FLAG_SOFTPLUS if softplus else 0, po,
-                                             on.handle))
-        return out
+    code = _code(u)
+    if u.dim() != 2:
+        raise ValueError(f"u must be [n_seq, dim], got {tuple(u.shape)}")
+    n_seq, views = u.shape[0], []
+    dim, G, N, ptrs = _scan_operands(index, u, delta, A, B, C, D, z, delta_bias, (n_seq,), views)
+    pp, n_pages = _pool(index, pages, n_seq, state)
+    ps = _need_ptr(state, "state", index, torch.float32, (n_pages, dim, N))
+    if out is None:
+        out = _out_like(u)
+    py = _row_ptr(out, "out", index, u.dtype, u.shape, views, 5)
+    strides = _strides(views, (dim,), (dim,), (G * N,), (G * N,), (dim,), (dim,)) if views else None
+    _check(lib().ttt_selective_scan_step(*ptrs, strides, ps, pp, n_pages, n_seq, dim, G, N, code,
+                                         TTT_FLAG_SOFTPLUS if softplus else 0, py, handle))
+    return out
 
 
-def ttt_selective_scan_backward(u, delta, A, B, C, d_out, ckpt, D=None, z=None, delta_bias=None, softplus: bool = True,
-                                d_state_out=None, state_in_grad: bool = False, cu_seqlens=None, workspace=None,
-                                stream=None):
+@_in_context
+def ttt_selective_scan_backward(index, handle, u, delta, A, B, C, d_out, ckpt, D=None, z=None, delta_bias=None,
+                                softplus: bool = True, d_state_out=None, state_in_grad: bool = False,
+                                cu_seqlens=None, workspace=None):
     """Gradients of ttt_selective_scan_forward for d_out (and d_state_out [n_seq, dim, d_state], the gradient
     of the states after each sequence), from the ckpt that the forward wrote.  Returns a dict: du, ddelta,
     dB, dC, dz (the activations' dtype; zero in rows outside every sequence), dA, dD, ddelta_bias float32, and
     dstate_in [n_seq, dim, d_state] with state_in_grad; None for inputs that are None."""
-    with _On(u, stream) as on:
-        n_seq, L, lead = _seq_sizes(u, "u", cu_seqlens)
-        packed, dt, dev = cu_seqlens is not None, u.dtype, on.device
-        rows = _Rows(on, dt)
-        dim, G, N, ptrs, c = _scan_operands(on, rows, u, delta, A, B, C, D, z, delta_bias, lead)
-        pd = rows(d_out, "d_out", u.shape)
-        if pd is None:
-            raise TypeError("d_out must be a torch.Tensor")
-        pc = _check_ckpt(on, ckpt, n_seq, L, dim, N, packed)
-        ps = on.ptr(d_state_out, "d_state_out", torch.float32, (n_seq, dim, N))
-        ws = on.workspace(ttt_selective_scan_backward_workspace_bytes(n_seq, L, dim, N, G, packed), workspace)
-        new = lambda shape: torch.empty(shape, dtype=dt, device=dev)
-        g = {"du": new(u.shape), "ddelta": new(u.shape), "dA": torch.empty((dim, N), device=dev), "dB": new(B.shape),
-             "dC": new(B.shape), "dD": None if D is None else torch.empty(dim, device=dev),
-             "dz": None if z is None else new(u.shape),
-             "ddelta_bias": None if delta_bias is None else torch.empty(dim, device=dev),
-             "dstate_in": torch.empty((n_seq, dim, N), device=dev) if state_in_grad else None}
-        _check(lib().ttt_selective_scan_backward(*ptrs, rows.strides(*(_packed_strides(c) if packed else c)),
-                                                 on.ptr(cu_seqlens, "cu_seqlens", torch.int32), pc, n_seq, L, dim, G, N,
-                                                 _dtype_code(u), (TTT_FLAG_SOFTPLUS if softplus else 0) | TTT_FLAG_ZERO_REST,
-                                                 pd, ps, g["du"].data_ptr(), g["ddelta"].data_ptr(), g["dA"].data_ptr(),
-                                                 g["dB"].data_ptr(), g["dC"].data_ptr(), _addr(g["dD"]), _addr(g["dz"]),
-                                                 _addr(g["ddelta_bias"]), _addr(g["dstate_in"]), ws.data_ptr(),
-                                                 ws.numel(), on.handle))
-        return g
+    code = _code(u)
+    n_seq, L, lead = _seq_sizes(u, "u", cu_seqlens)
+    packed, views = cu_seqlens is not None, []
+    dim, G, N, ptrs = _scan_operands(index, u, delta, A, B, C, D, z, delta_bias, lead, views)
+    pd = _row_ptr(d_out, "d_out", index, u.dtype, u.shape, views, 5)
+    pk = _ckpt_ptr(ckpt, index, n_seq, L, dim, N, packed)
+    ps = _maybe_ptr(d_state_out, "d_state_out", index, torch.float32, (n_seq, dim, N))
+    pc = _cu_ptr(cu_seqlens, index)
+    ws = _space(ttt_selective_scan_backward_workspace_bytes(n_seq, L, dim, N, G, packed), workspace, index)
+    g = {"du": _out_like(u), "ddelta": _out_like(u), "dA": _f32((dim, N), u), "dB": _out_like(B), "dC": _out_like(C),
+         "dD": None if D is None else _f32((dim,), u), "dz": None if z is None else _out_like(u),
+         "ddelta_bias": None if delta_bias is None else _f32((dim,), u),
+         "dstate_in": _f32((n_seq, dim, N), u) if state_in_grad else None}
+    _check(lib().ttt_selective_scan_backward(*ptrs, _scan_strides(views, L, dim, G, N), pc, pk, n_seq, L, dim, G, N, code,
+                                             (TTT_FLAG_SOFTPLUS if softplus else 0) | TTT_FLAG_ZERO_REST, pd, ps,
+                                             g["du"].data_ptr(), g["ddelta"].data_ptr(), g["dA"].data_ptr(),
+                                             g["dB"].data_ptr(), g["dC"].data_ptr(), _addr(g["dD"]), _addr(g["dz"]),
+                                             _addr(g["ddelta_bias"]), _addr(g["dstate_in"]), ws.data_ptr(), ws.numel(),
+                                             handle))
+    return g
 
 
-def _cache_tensors(on, tensors, n_pages):
+def _cache_tensors(index, tensors, n_pages=None):
+    """The ABI's arrays of the cache's tensors, each [n_pages, ...]."""
+    if not isinstance(tensors, (list, tuple)):
+        raise TypeError("tensors must be a list of the cache's tensors")
     n = len(tensors)
+    if n_pages is None:
+        if not n or not isinstance(tensors[0], torch.Tensor) or tensors[0].dim() < 1:
+            raise ValueError("tensors must name at least one tensor of pages")
+        n_pages = tensors[0].shape[0]
     ptrs, sizes = (ctypes.c_void_p * max(1, n))(), (ctypes.c_longlong * max(1, n))()
     for k, t in enumerate(tensors):
-        ptrs[k] = on.need(t, "a page tensor")
+        if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.is_contiguous()):
+            _refuse(t, f"tensors[{k}]", index, None, None)
         if t.dim() < 1 or t.shape[0] != n_pages:
             raise ValueError(f"tensors[{k}] must have {n_pages} pages (its first dimension), got {tuple(t.shape)}")
-        sizes[k] = t.numel() // n_pages * t.element_size()
+        ptrs[k] = t.data_ptr()
+        sizes[k] = t.numel() // max(1, n_pages) * t.element_size()
     return ptrs, sizes, n, n_pages
 
 
-def _books(on, table, owner):
-    n_rows, n_pages = table.numel(), owner.numel()
-    return on.need(table, "table", torch.int32, (n_rows,)), n_rows, on.need(owner, "owner", torch.int32, (n_pages,)), n_pages
+def _i32_ptr(t, name, index, n=None):
+    shape = (n,) if n is not None else ((t.numel(),) if isinstance(t, torch.Tensor) else None)
+    return _need_ptr(t, name, index, torch.int32, shape)
+
+
+def _i32(like, *sizes):
+    """Pieces of one int32 buffer."""
+    return torch.empty(sum(sizes), dtype=torch.int32, device=like.device).split(sizes)
 
 
 def ttt_cache_copy(tensors, src, dst, stream=None):
     """Copy pages: page dst[i] of every tensor (each [n_pages, ...]) becomes page src[i].  Returns copied
     (int32 [n]): 0 where a pair was refused (an index outside the cache, a destination named before or
     also named as a source)."""
-    with _On(src, stream) as on:
-        if not tensors:
-            raise ValueError("tensors must name at least one tensor")
-        n = src.numel()
-        ps, pd = on.need(src, "src", torch.int32, (n,)), on.need(dst, "dst", torch.int32, (n,))
-        t = _cache_tensors(on, tensors, tensors[0].shape[0])
-        copied, ws = torch.empty(3 * n + 1, dtype=torch.int32, device=on.device).split((n, 2 * n + 1))
-        _check(lib().ttt_cache_copy(*t, ps, pd, n, copied.data_ptr(), ws.data_ptr(), on.handle))
-        return copied
+    return _cache_copy(src, tensors, dst, stream=stream)
+
+
+@_in_context
+def _cache_copy(index, handle, src, tensors, dst):
+    t = _cache_tensors(index, tensors)
+    ps = _i32_ptr(src, "src", index)
+    n = src.numel()
+    pd = _i32_ptr(dst, "dst", index, n)
+    copied, ws = _i32(src, n, 2 * n + 1)
+    _check(lib().ttt_cache_copy(*t, ps, pd, n, copied.data_ptr(), ws.data_ptr(), handle))
+    return copied
 
 
 def ttt_cache_fork(tensors, table, owner, parents, children, stream=None):
@@ -999,33 +1026,42 @@ def ttt_cache_fork(tensors, table, owner, parents, children, stream=None):
     a parent of -1: a new sequence).  table: int32 [n_rows], the page of each sequence row; owner: int32
     [n_pages], the row of each page; both -1 where there is none, and updated in place.  Returns pages
     (int32 [n]): the page given to each request, or -1."""
-    with _On(table, stream) as on:
-        n = children.numel()
-        pt, n_rows, po, n_pages = _books(on, table, owner)
-        pp, pc = on.need(parents, "parents", torch.int32, (n,)), on.need(children, "children", torch.int32, (n,))
-        t = _cache_tensors(on, tensors, n_pages)
-        pages, ws = torch.empty(3 * n + 1, dtype=torch.int32, device=on.device).split((n, 2 * n + 1))
-        _check(lib().ttt_cache_fork(*t, pt, n_rows, po, pp, pc, n, pages.data_ptr(), ws.data_ptr(), on.handle))
-        return pages
+    return _cache_fork(table, tensors, owner, parents, children, stream=stream)
 
 
-def ttt_cache_free(table, owner, rows, stream=None):
+@_in_context
+def _cache_fork(index, handle, table, tensors, owner, parents, children):
+    pt, po = _i32_ptr(table, "table", index), _i32_ptr(owner, "owner", index)
+    pc = _i32_ptr(children, "children", index)
+    n = children.numel()
+    pp = _i32_ptr(parents, "parents", index, n)
+    t = _cache_tensors(index, tensors, owner.numel())
+    pages, ws = _i32(table, n, 2 * n + 1)
+    _check(lib().ttt_cache_fork(*t, pt, table.numel(), po, pp, pc, n, pages.data_ptr(), ws.data_ptr(), handle))
+    return pages
+
+
+@_in_context
+def ttt_cache_free(index, handle, table, owner, rows):
     """Free the pages of the sequence rows (int32 [n]).  Returns the number freed (an int32 tensor)."""
-    with _On(table, stream) as on:
-        n = rows.numel()
-        books = _books(on, table, owner)
-        freed = torch.empty((), dtype=torch.int32, device=on.device)
-        _check(lib().ttt_cache_free(*books, on.need(rows, "rows", torch.int32, (n,)), n, freed.data_ptr(), on.handle))
-        return freed
+    pt, po, pr = _i32_ptr(table, "table", index), _i32_ptr(owner, "owner", index), _i32_ptr(rows, "rows", index)
+    freed = torch.empty((), dtype=torch.int32, device=table.device)
+    _check(lib().ttt_cache_free(pt, table.numel(), po, owner.numel(), pr, rows.numel(), freed.data_ptr(), handle))
+    return freed
 
 
 def ttt_cache_compact(tensors, table, owner, stream=None):
     """Move the live pages to the front, so that the first `live` pages are a dense batch for the decode
     steps.  Returns (live, new_page): the number of live pages (an int32 tensor) and the new page of each
     old one (int32 [n_pages], -1 where it was free)."""
-    with _On(table, stream) as on:
-        pt, n_rows, po, n_pages = _books(on, table, owner)
-        t = _cache_tensors(on, tensors, n_pages)
-        live, new_page, ws = torch.empty(2 * n_pages + 3, dtype=torch.int32, device=on.device).split((1, n_pages, n_pages + 2))
-        _check(lib().ttt_cache_compact(*t, pt, n_rows, po, live.data_ptr(), new_page.data_ptr(), ws.data_ptr(), on.handle))
-        return live[0], new_page
+    return _cache_compact(table, tensors, owner, stream=stream)
+
+
+@_in_context
+def _cache_compact(index, handle, table, tensors, owner):
+    pt, po = _i32_ptr(table, "table", index), _i32_ptr(owner, "owner", index)
+    n_pages = owner.numel()
+    t = _cache_tensors(index, tensors, n_pages)
+    live, new_page, ws = _i32(table, 1, n_pages, n_pages + 2)
+    _check(lib().ttt_cache_compact(*t, pt, table.numel(), po, live.data_ptr(), new_page.data_ptr(), ws.data_ptr(), handle))
+    return live[0], new_page

@@ -73,18 +73,17 @@ __device__ __forceinline__ void zero_piece(char* dst, long long bytes) {
 }
 
 // moves[0] pairs (source, destination) from moves[1] on; a source of -1 zeroes the destination.
-__global__ void __launch_bounds__(kCopy) cache_copy_kernel(const CacheTensors t, const int* moves, int pieces) {
-    const int n = moves[0];
+__global__ void __launch_bounds__(kCopy) cache_copy_kernel(const __grid_constant__ CacheTensors t, const int* moves) {
+    const int n = moves[0], pieces = t.first[t.n];
     const long long total = static_cast<long long>(n) * pieces;
     for (long long w = blockIdx.x; w < total; w += gridDim.x) {
         const int pair = static_cast<int>(w / pieces);
-        int piece = static_cast<int>(w % pieces);
-        int k = 0;
-        for (; k < t.n; ++k) {  // the tensor this piece belongs to
-            const int m = static_cast<int>((t.bytes[k] + kPiece - 1) / kPiece);
-            if (piece < m) break;
-            piece -= m;
+        int piece = static_cast<int>(w % pieces), k = 0, hi = t.n - 1;
+        while (k < hi) {  // the tensor this piece belongs to: the last whose first piece is not behind it
+            const int mid = (k + hi + 1) >> 1;
+            if (t.first[mid] <= piece) k = mid; else hi = mid - 1;
         }
+        piece -= t.first[k];
         const long long off = piece * kPiece, bytes = min(kPiece, t.bytes[k] - off);
         const int from = moves[1 + 2 * pair], to = moves[2 + 2 * pair];
         char* dst = t.base[k] + to * t.bytes[k] + off;
@@ -251,36 +250,36 @@ __global__ void __launch_bounds__(kBook) cache_compact_kernel(const CacheArgs a)
     }
 }
 
-cudaError_t copy_moves(const CacheArgs& a, int most, cudaStream_t s) {
-    long long pieces = 0;
-    for (int k = 0; k < a.t.n; ++k) pieces += (a.t.bytes[k] + kPiece - 1) / kPiece;
-    if (pieces == 0 || most == 0) return cudaSuccess;
-    const long long want = pieces * most;
+cudaError_t copy_moves(CacheTensors& t, const CacheArgs& a, int most, cudaStream_t s) {
+    t.first[0] = 0;
+    for (int k = 0; k < t.n; ++k) t.first[k + 1] = t.first[k] + static_cast<int>((t.bytes[k] + kPiece - 1) / kPiece);
+    const long long want = static_cast<long long>(t.first[t.n]) * most;
+    if (want == 0) return cudaSuccess;
     const unsigned grid = static_cast<unsigned>(want < 148 * 8 ? want : 148 * 8);  // 8 blocks of 256 threads an SM
-    cache_copy_kernel<<<grid, kCopy, 0, s>>>(a.t, a.moves, static_cast<int>(pieces));
+    cache_copy_kernel<<<grid, kCopy, 0, s>>>(t, a.moves);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_cache_copy(const CacheArgs& a, cudaStream_t s) {
+cudaError_t launch_cache_copy(const CacheArgs& a, CacheTensors& t, cudaStream_t s) {
     cache_pairs_kernel<<<1, kBook, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess ? e : copy_moves(a, a.n, s);
+    return e != cudaSuccess ? e : copy_moves(t, a, a.n, s);
 }
-cudaError_t launch_cache_fork(const CacheArgs& a, cudaStream_t s) {
+cudaError_t launch_cache_fork(const CacheArgs& a, CacheTensors& t, cudaStream_t s) {
     cache_fork_kernel<<<1, kBook, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess ? e : copy_moves(a, a.n, s);
+    return e != cudaSuccess ? e : copy_moves(t, a, a.n, s);
 }
 cudaError_t launch_cache_free(const CacheArgs& a, cudaStream_t s) {
     cache_free_kernel<<<1, kBook, 0, s>>>(a);
     return cudaGetLastError();
 }
-cudaError_t launch_cache_compact(const CacheArgs& a, cudaStream_t s) {
+cudaError_t launch_cache_compact(const CacheArgs& a, CacheTensors& t, cudaStream_t s) {
     cache_compact_kernel<<<1, kBook, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess ? e : copy_moves(a, a.n_pages / 2, s);
+    return e != cudaSuccess ? e : copy_moves(t, a, a.n_pages / 2, s);
 }
 
 }  // namespace ttt

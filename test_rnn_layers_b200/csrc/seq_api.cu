@@ -1,6 +1,8 @@
 // seq_api.cu -- the extern "C" entry points of the causal convolution, the selective scan and the
 // cache's page operations (declared in include/ttt.h).  Arguments are checked on the host before any
 // CUDA call; no device memory is allocated here.
+#include <algorithm>
+
 #include "api_util.h"
 #include "seq_internal.h"
 
@@ -547,13 +549,22 @@ int check_tensors(void* const* tensors, const long long* page_bytes, int n_tenso
     return TTT_OK;
 }
 
-// No tensor may overlap another or one of `books`, nor the books one another.
+// No tensor may overlap another, one of the `books` (written) or one of the `reads`, nor the books one
+// another or the reads.
 int check_apart(const ttt::CacheTensors& t, int n_pages, const Span* books, int n_books, const Span* reads, int n_reads) {
-    Span outs[ttt::kCacheMaxTensors + 4];
+    Span all[ttt::kCacheMaxTensors + 5];
     int n = 0;
-    for (int i = 0; i < t.n; ++i) outs[n++] = {"a page tensor", t.base[i], static_cast<size_t>(t.bytes[i]) * n_pages};
-    for (int i = 0; i < n_books; ++i) outs[n++] = books[i];
-    return check_aliasing(reads, n_reads, outs, n);
+    for (int i = 0; i < t.n; ++i) all[n++] = {"a page tensor", t.base[i], static_cast<size_t>(t.bytes[i]) * n_pages};
+    for (int i = 0; i < n_books; ++i) all[n++] = books[i];
+    for (int r = 0; r < n_reads; ++r)
+        for (int i = 0; i < n; ++i)
+            if (ttt::overlaps(all[i], reads[r])) return fail(TTT_ERR_ALIAS, "%s overlaps %s", all[i].name, reads[r].name);
+    std::sort(all, all + n, [](const Span& x, const Span& y) {
+        return reinterpret_cast<uintptr_t>(x.p) < reinterpret_cast<uintptr_t>(y.p);
+    });
+    for (int i = 1; i < n; ++i)  // in the order of their starts, of two that overlap the first overlaps its neighbour
+        if (ttt::overlaps(all[i - 1], all[i])) return fail(TTT_ERR_ALIAS, "%s and %s overlap", all[i - 1].name, all[i].name);
+    return TTT_OK;
 }
 
 }  // namespace
@@ -561,7 +572,8 @@ int check_apart(const ttt::CacheTensors& t, int n_pages, const Span* books, int 
 int ttt_cache_copy(void* const* tensors, const long long* page_bytes, int n_tensors, int n_pages, const int* src,
                    const int* dst, int n, int* copied, int* workspace, void* stream) {
     ttt::CacheArgs a{};
-    TTT_TRY(check_tensors(tensors, page_bytes, n_tensors, n_pages, &a.t));
+    ttt::CacheTensors t;
+    TTT_TRY(check_tensors(tensors, page_bytes, n_tensors, n_pages, &t));
     if (n < 0 || n > n_pages) return fail(TTT_ERR_ARG, "n must be in [0, n_pages] (got %d of %d)", n, n_pages);
     if (n == 0) return ok();
     TTT_TRY(need("src", src, 4));
@@ -570,9 +582,9 @@ int ttt_cache_copy(void* const* tensors, const long long* page_bytes, int n_tens
     TTT_TRY(need("workspace", workspace, 4));
     const Span reads[] = {{"src", src, n * 4ull}, {"dst", dst, n * 4ull}};
     const Span books[] = {{"copied", copied, n * 4ull}, {"workspace", workspace, (1 + 2ull * n) * 4}};
-    TTT_TRY(check_apart(a.t, n_pages, books, 2, reads, 2));
+    TTT_TRY(check_apart(t, n_pages, books, 2, reads, 2));
     a.n_pages = n_pages; a.n = n; a.a = src; a.b = dst; a.result = copied; a.moves = workspace;
-    const cudaError_t e = ttt::launch_cache_copy(a, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = ttt::launch_cache_copy(a, t, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ok() : cuda_fail(e, "ttt_cache_copy launch");
 }
 
@@ -580,7 +592,8 @@ int ttt_cache_fork(void* const* tensors, const long long* page_bytes, int n_tens
                    int n_rows, int* owner, const int* parents, const int* children, int n, int* pages, int* workspace,
                    void* stream) {
     ttt::CacheArgs a{};
-    TTT_TRY(check_tensors(tensors, page_bytes, n_tensors, n_pages, &a.t));
+    ttt::CacheTensors t;
+    TTT_TRY(check_tensors(tensors, page_bytes, n_tensors, n_pages, &t));
     if (n_rows < 1) return fail(TTT_ERR_ARG, "n_rows must be >= 1 (got %d)", n_rows);
     if (n < 0 || n > (1 << 24)) return fail(TTT_ERR_ARG, "n must be in [0, 2^24] (got %d)", n);
     TTT_TRY(need("table", table, 4));
@@ -593,10 +606,10 @@ int ttt_cache_fork(void* const* tensors, const long long* page_bytes, int n_tens
     const Span reads[] = {{"parents", parents, n * 4ull}, {"children", children, n * 4ull}};
     const Span books[] = {{"table", table, n_rows * 4ull}, {"owner", owner, n_pages * 4ull}, {"pages", pages, n * 4ull},
                           {"workspace", workspace, (1 + 2ull * n) * 4}};
-    TTT_TRY(check_apart(a.t, n_pages, books, 4, reads, 2));
+    TTT_TRY(check_apart(t, n_pages, books, 4, reads, 2));
     a.n_pages = n_pages; a.n_rows = n_rows; a.n = n; a.table = table; a.owner = owner; a.a = parents; a.b = children;
     a.result = pages; a.moves = workspace;
-    const cudaError_t e = ttt::launch_cache_fork(a, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = ttt::launch_cache_fork(a, t, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ok() : cuda_fail(e, "ttt_cache_fork launch");
 }
 
@@ -619,25 +632,20 @@ int ttt_cache_free(int* table, int n_rows, int* owner, int n_pages, const int* r
 int ttt_cache_compact(void* const* tensors, const long long* page_bytes, int n_tensors, int n_pages, int* table,
                       int n_rows, int* owner, int* live, int* new_page, int* workspace, void* stream) {
     ttt::CacheArgs a{};
-    TTT_TRY(check_tensors(tensors, page_bytes, n_tensors, n_pages, &a.t));
+    ttt::CacheTensors t;
+    TTT_TRY(check_tensors(tensors, page_bytes, n_tensors, n_pages, &t));
     if (n_rows < 1) return fail(TTT_ERR_ARG, "n_rows must be >= 1 (got %d)", n_rows);
     TTT_TRY(need("table", table, 4));
     TTT_TRY(need("owner", owner, 4));
     TTT_TRY(need("live", live, 4));
     TTT_TRY(need("new_page", new_page, 4));
     TTT_TRY(need("workspace", workspace, 4));
-    Span outs[ttt::kCacheMaxTensors + 5];
-    int k = 0;
-    for (int i = 0; i < a.t.n; ++i) outs[k++] = {"a page tensor", a.t.base[i], static_cast<size_t>(a.t.bytes[i]) * n_pages};
-    outs[k++] = {"table", table, n_rows * 4ull};
-    outs[k++] = {"owner", owner, n_pages * 4ull};
-    outs[k++] = {"live", live, 4};
-    outs[k++] = {"new_page", new_page, n_pages * 4ull};
-    outs[k++] = {"workspace", workspace, (2 + static_cast<size_t>(n_pages)) * 4};
-    TTT_TRY(check_aliasing(nullptr, 0, outs, k));
+    const Span books[] = {{"table", table, n_rows * 4ull}, {"owner", owner, n_pages * 4ull}, {"live", live, 4},
+                          {"new_page", new_page, n_pages * 4ull}, {"workspace", workspace, (2 + static_cast<size_t>(n_pages)) * 4}};
+    TTT_TRY(check_apart(t, n_pages, books, 5, nullptr, 0));
     a.n_pages = n_pages; a.n_rows = n_rows; a.table = table; a.owner = owner; a.result = new_page; a.count = live;
     a.moves = workspace;
-    const cudaError_t e = ttt::launch_cache_compact(a, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = ttt::launch_cache_compact(a, t, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ok() : cuda_fail(e, "ttt_cache_compact launch");
 }
 

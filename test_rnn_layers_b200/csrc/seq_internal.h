@@ -112,14 +112,14 @@ struct ScanBwdArgs {
     int wide;                    // bits: the rows of u, delta, z, d_out, du, d delta, dz start on 16-byte boundaries
 };
 
-constexpr int kCacheMaxTensors = 64;
-struct CacheTensors {
+constexpr int kCacheMaxTensors = 512;
+struct CacheTensors {                    // a parameter of the copying kernel: 10 KB of its 32
     int n;
+    int first[kCacheMaxTensors + 1];     // the first of each tensor's pieces; their number at [n]
     char* base[kCacheMaxTensors];
     long long bytes[kCacheMaxTensors];   // per page
 };
 struct CacheArgs {
-    CacheTensors t;
     int n_pages, n_rows, n;
     int* table;                  // [n_rows]
     int* owner;                  // [n_pages]
@@ -141,9 +141,9 @@ cudaError_t launch_scan(const ScanArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_scan_step(const ScanStepArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_scan_bwd(const ScanBwdArgs& a, int dtype, cudaStream_t s);
 
-cudaError_t launch_cache_copy(const CacheArgs& a, cudaStream_t s);
-cudaError_t launch_cache_fork(const CacheArgs& a, cudaStream_t s);
+cudaError_t launch_cache_copy(const CacheArgs& a, CacheTensors& t, cudaStream_t s);
+cudaError_t launch_cache_fork(const CacheArgs& a, CacheTensors& t, cudaStream_t s);
 cudaError_t launch_cache_free(const CacheArgs& a, cudaStream_t s);
-cudaError_t launch_cache_compact(const CacheArgs& a, cudaStream_t s);
+cudaError_t launch_cache_compact(const CacheArgs& a, CacheTensors& t, cudaStream_t s);
 
 }  // namespace ttt

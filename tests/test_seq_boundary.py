@@ -146,7 +146,7 @@ def cache(lib, what, tensors=((A, 256), (2 * A, 64)), n_pages=10, n_rows=6, n=4,
 
 @pytest.mark.parametrize("what,kw,code", [
     ("copy", dict(n_pages=0), -1), ("copy", dict(n=11), -1), ("copy", dict(n=-1), -1), ("copy", dict(a=None), -1), ("copy", dict(out=None), -1),
-    ("copy", dict(tensors=((A, 0),)), -1), ("copy", dict(tensors=((None, 4),)), -1), ("copy", dict(tensors=((A, 4),) * 65), -6),
+    ("copy", dict(tensors=((A, 0),)), -1), ("copy", dict(tensors=((None, 4),)), -1), ("copy", dict(tensors=((A, 4),) * 513), -6),
     ("copy", dict(tensors=((A, 64), (A + 64, 64))), -3), ("copy", dict(out=5 * A), -3), ("copy", dict(ws=A), -3), ("copy", dict(ws=9 * A + 2), -2),
     ("fork", dict(table=None), -1), ("fork", dict(owner=None), -1), ("fork", dict(n_rows=0), -1), ("fork", dict(n=-1), -1), ("fork", dict(b=None), -1),
     ("fork", dict(b=6 * A + 1), -2), ("fork", dict(table=4 * A), -3), ("fork", dict(out=6 * A), -3), ("fork", dict(a=2 * A), -3),

@@ -322,14 +322,33 @@ def test_autograd_in_a_graph(libttt):
     assert all(torch.equal(a, b) for a, b in zip(held, want))
 
 
+def test_a_cache_of_many_tensors(libttt):
+    """All layers' states in one call: 24 layers of 4 tensors, one of them with pages of odd sizes."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    pool = [torch.randn(9, 3 + k % 7 * 40, device="cuda", generator=g) for k in range(96)]
+    pool[50] = torch.randint(0, 255, (9, 333), device="cuda", generator=g, dtype=torch.uint8)
+    before = [t.clone() for t in pool]
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    table, owner = i32([8, 2, -1, -1, -1]), i32([-1, -1, 1, -1, -1, -1, -1, -1, 0])
+    assert libttt.ttt_cache_fork(pool, table, owner, i32([0, -1]), i32([3, 4])).tolist() == [0, 1]
+    live, new = libttt.ttt_cache_compact(pool, table, owner)
+    assert int(live) == 4 and new.tolist() == [0, 1, 2, -1, -1, -1, -1, -1, 3] and owner.tolist() == [3, 4, 1, 0] + [-1] * 5
+    for t, b in zip(pool, before):
+        assert torch.equal(t[0], b[8]) and (t[1] == 0).all() and torch.equal(t[2], b[2]) and torch.equal(t[3], b[8])
+    with pytest.raises(libttt.TTTError):
+        libttt.ttt_cache_fork(pool * 6, table, owner, i32([0]), i32([2]))
+
+
 def test_binding_refuses(libttt):
     x, w = torch.randn(2, 8, 12, device="cuda"), torch.randn(12, 4, device="cuda")
+    assert torch.equal(libttt.ttt_causal_conv_forward(x=x, weight=w), libttt.ttt_causal_conv_forward(x, w))  # by name, too
     for bad in (dict(x=x.half()), dict(x=x[0]), dict(x=x.transpose(1, 2)), dict(weight=w.bfloat16()), dict(weight=w[:5]), dict(weight=w.cpu()),
                 dict(x=x.cpu()), dict(bias=w[0]), dict(out=x[:1]), dict(state_in=x), dict(pages=torch.zeros(2, dtype=torch.int64, device="cuda"))):
         with pytest.raises((TypeError, ValueError)):
             libttt.ttt_causal_conv_forward(**(dict(x=x, weight=w) | bad))
     u, A = x, -torch.rand(12, 16, device="cuda")
     B = torch.randn(2, 8, 1, 16, device="cuda")
+    assert libttt.ttt_selective_scan_forward(u=u, delta=u, A=A, B=B, C=B).shape == u.shape
     for bad in (dict(delta=x[:, :4]), dict(A=A[:5]), dict(B=B[:, :, 0]), dict(C=B.bfloat16()), dict(D=w), dict(z=x.bfloat16()),
                 dict(state_in=A), dict(ckpt=torch.empty(8, device="cuda")), dict(C=None), dict(delta=None)):
         with pytest.raises((TypeError, ValueError)):
