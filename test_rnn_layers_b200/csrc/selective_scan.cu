@@ -315,43 +315,84 @@ __global__ void __launch_bounds__(Y::THREADS) scan_kernel(const ScanArgs a) {
     }
 }
 
+struct pair4 {
+    f32x2 lo, hi;
+};
+
 // One token of each sequence, the state in its page read and written once: 8 N bytes a channel,
-// which is what bounds it.  P lanes a channel, as above.
+// which is what bounds it.  P neighbouring lanes share a channel, 4 states each, and take P sequences
+// together: lane q prepares and finishes sequence q of them (its dt, dt u and gate), so that this is done
+// once a channel and sequence and not once a lane.
 template <typename T, int P, bool PAD>
 __global__ void __launch_bounds__(256) scan_step_kernel(const ScanStepArgs a) {
-    const long long id = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / P;
-    const int q = threadIdx.x % P, b = static_cast<int>(id / a.dim), d = static_cast<int>(id % a.dim);
-    const int page = b < a.n_seq ? page_of(a.pages, a.n_pages, b) : -1;
-    const bool on = page >= 0;
-    float y = 0.f, u = 0.f;
-    if (on) {
-        const int left = a.N - 4 * q, g = d / (a.dim / a.groups), n = g * a.N + 4 * q;
-        float* hp = a.state + (static_cast<long long>(page) * a.dim + d) * a.N + 4 * q;
-        float h[4], A[4];
-        load_state<4, PAD>(hp, left, h);
-        load_state<4, PAD>(a.A + static_cast<long long>(d) * a.N + 4 * q, left, A);
-        u = to_f32(static_cast<const T*>(a.u)[b * a.su + d]);
-        float dt = to_f32(static_cast<const T*>(a.delta)[b * a.sdt + d]) + (a.bias ? a.bias[d] : 0.f);
-        if (a.softplus) dt = softplus_f(dt);
-        const T* Bm = static_cast<const T*>(a.B) + b * a.sB + n;
-        const T* Cm = static_cast<const T*>(a.C) + b * a.sC + n;
+    const int q = threadIdx.x % P, d0 = (blockIdx.x * 256 + threadIdx.x) / P;
+    const bool live = d0 < a.dim;
+    const int d = live ? d0 : a.dim - 1, left = a.N - 4 * q;
+    const long long hoff = static_cast<long long>(d) * a.N + 4 * q, hrow = static_cast<long long>(a.dim) * a.N;
+    const int n = (a.groups == 1 ? 0 : d / (a.dim / a.groups) * a.N) + 4 * q;
+    float A[4];
+    load_state<4, PAD>(a.A + hoff, left, A);
+    const f32x2 A2[2] = {mul2(pack2(A[0], A[1]), both(kLog2e)), mul2(pack2(A[2], A[3]), both(kLog2e))};
+    const float bias = a.bias ? a.bias[d] : 0.f, Dk = a.D ? a.D[d] : 0.f;
+    auto four = [&](const void* base, long long stride, int b) {
+        const T* p = static_cast<const T*>(base) + b * stride + n;
+        float v[4];
+        if (!PAD && a.wide) {
+            load_vec<4>(p, v);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (!PAD || i < left) {
-                h[i] = fmaf(decay2(dt * (A[i] * kLog2e)), h[i], dt * u * to_f32(Bm[i]));
-                y = fmaf(to_f32(Cm[i]), h[i], y);
+            for (int i = 0; i < 4; ++i) v[i] = !PAD || i < left ? to_f32(p[i]) : 0.f;
+        }
+        return pair4{pack2(v[0], v[1]), pack2(v[2], v[3])};
+    };
+    for (int b0 = blockIdx.y * P; b0 < a.n_seq; b0 += gridDim.y * P) {
+        const int bq = b0 + q;
+        const bool in = live && bq < a.n_seq;
+        const int page = in ? page_of(a.pages, a.n_pages, bq) : -1;
+        float u = 0.f, dt = 0.f, z = 0.f, y[P];
+        if (in) {
+            u = to_f32(static_cast<const T*>(a.u)[bq * a.su + d]);
+            dt = to_f32(static_cast<const T*>(a.delta)[bq * a.sdt + d]) + bias;
+            if (a.z) z = to_f32(static_cast<const T*>(a.z)[bq * a.sz + d]);
+            if (a.softplus) dt = softplus_f(dt);
+        }
+        const float du = dt * u;
+        float h[P][4];
+        int pg[P];
+#pragma unroll
+        for (int j = 0; j < P; ++j) {  // all the states on their way before the first is used
+            pg[j] = __shfl_sync(0xffffffffu, page, j, P);
+            if (pg[j] >= 0) load_state<4, PAD>(a.state + pg[j] * hrow + hoff, left, h[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            const float dtj = __shfl_sync(0xffffffffu, dt, j, P), duj = __shfl_sync(0xffffffffu, du, j, P);
+            y[j] = 0.f;
+            if (pg[j] >= 0) {
+                const pair4 b = four(a.B, a.sB, b0 + j), cc = four(a.C, a.sC, b0 + j);
+                f32x2 h0 = pack2(h[j][0], h[j][1]), h1 = pack2(h[j][2], h[j][3]);
+                h0 = fma2(decay2(mul2(both(dtj), A2[0])), h0, mul2(both(duj), b.lo));
+                h1 = fma2(decay2(mul2(both(dtj), A2[1])), h1, mul2(both(duj), b.hi));
+                unpack2(h0, h[j][0], h[j][1]);
+                unpack2(h1, h[j][2], h[j][3]);
+                if (PAD) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) h[j][i] = i < left ? h[j][i] : 0.f;
+                    h0 = pack2(h[j][0], h[j][1]);
+                    h1 = pack2(h[j][2], h[j][3]);
+                }
+                store_state<4, PAD>(a.state + pg[j] * hrow + hoff, left, h[j]);
+                float lo, hi;
+                unpack2(fma2(cc.hi, h1, mul2(cc.lo, h0)), lo, hi);
+                y[j] = lo + hi;
             }
         }
-        store_state<4, PAD>(hp, left, h);
-    }
-#pragma unroll
-    for (int w = P / 2; w >= 1; w /= 2) y += __shfl_xor_sync(0xffffffffu, y, w);
-    if (b < a.n_seq && q == 0) {
-        if (on) {
-            y = fmaf(a.D ? a.D[d] : 0.f, u, y);
-            if (a.z) y *= silu_f(to_f32(static_cast<const T*>(a.z)[b * a.sz + d]));
+        float out = reduce_across<P, 1>(y, q);
+        if (in) {
+            out = fmaf(Dk, u, out);
+            if (a.z) out *= silu_f(z);
+            static_cast<T*>(a.out)[bq * a.so + d] = from_f32<T>(page >= 0 ? out : 0.f);
         }
-        static_cast<T*>(a.out)[b * a.so + d] = from_f32<T>(y);
     }
 }
 
@@ -370,8 +411,8 @@ cudaError_t run(const ScanArgs& a, cudaStream_t s) {
 }
 template <typename T, int P, bool PAD>
 cudaError_t run_step(const ScanStepArgs& a, cudaStream_t s) {
-    const long long n = static_cast<long long>(a.n_seq) * a.dim * P;
-    scan_step_kernel<T, P, PAD><<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(a);
+    const int most = (a.n_seq + P - 1) / P;
+    scan_step_kernel<T, P, PAD><<<dim3((a.dim + 256 / P - 1) / (256 / P), most < 65535 ? most : 65535), 256, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -425,7 +466,10 @@ cudaError_t launch_scan(const ScanArgs& args, int dtype, cudaStream_t s) {
     return dtype == 0 ? dispatch<float>(a, s) : dispatch<__nv_bfloat16>(a, s);
 }
 
-cudaError_t launch_scan_step(const ScanStepArgs& a, int dtype, cudaStream_t s) {
+cudaError_t launch_scan_step(const ScanStepArgs& args, int dtype, cudaStream_t s) {
+    ScanStepArgs a = args;
+    const size_t esz = dtype == 0 ? 4 : 2;  // B and C four states a load where each lane's start on such a boundary
+    a.wide = (reinterpret_cast<uintptr_t>(a.B) | reinterpret_cast<uintptr_t>(a.C) | a.sB * esz | a.sC * esz | a.N * esz) % (4 * esz) == 0;
     return dtype == 0 ? dispatch_step<float>(a, s) : dispatch_step<__nv_bfloat16>(a, s);
 }
 

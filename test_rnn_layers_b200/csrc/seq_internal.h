@@ -89,6 +89,7 @@ struct ScanStepArgs {
     const int* pages;
     int n_pages;
     void* out;
+    int wide;                    // 1: B and C can be read four states at a time
 };
 
 struct ScanBwdArgs {
