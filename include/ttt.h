@@ -1,6 +1,7 @@
 /*
  * ttt.h -- C ABI of libttt.so: the TTT-Linear / TTT-MLP mini-batch test-time-training scan
- * and the TTT-Linear cache decode step, for NVIDIA B200 (sm_100a).
+ * and the TTT-Linear cache decode step, the short causal convolution and the selective state space
+ * scan, and the pages of a cache of recurrent states, for NVIDIA B200 (sm_100a).
  *
  * Sources, cited by page title and section:
  *   [walkthrough] "代码连连看——TTT" (jiafeimiao.top): TTTBase.forward, TTTLinear.ttt and

@@ -1,4 +1,5 @@
-"""Python binding of libttt.so: the TTT-Linear / TTT-MLP scan and the decode step on B200.
+"""Python binding of libttt.so: the TTT-Linear / TTT-MLP scan and the decode step, the causal convolution, the
+selective scan and the pages of a cache of recurrent states on B200.
 
 Argument marshalling only -- every step of the computation runs in the library's CUDA kernels.
 PyTorch supplies device memory and the current stream.  The functions carry the C-ABI names
