@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(Y::THREADS) scan_kernel(const ScanArgs a) {
 #pragma unroll
                     for (int i = 0; i < S / 2; ++i) f[m][j][i] = decay2(mul2(dt, A2[m][i]));
                 }
+            __syncwarp();  // (here and below: loads do not move across, 2 % faster)
 #pragma unroll
             for (int j = 0; j < kScanChunk; ++j) {
                 const int t = t1 + j;
@@ -270,6 +271,7 @@ __global__ void __launch_bounds__(Y::THREADS) scan_kernel(const ScanArgs a) {
                     }
                 }
             }
+            __syncwarp();
             if (OUT) {
 #pragma unroll
                 for (int m = 0; m < R; ++m)
@@ -463,6 +465,9 @@ bool rows_on_16(const void* p, RowStride r, const ScanArgs& a, size_t esz) {
 }  // namespace
 
 int scan_channels(int N) { return lanes_channels(N); }
+int scan_warps(int N) {
+    return N <= 4 ? Lanes4::NW : N <= 8 ? Lanes8::NW : N <= 16 ? Lanes16::NW : N <= 32 ? Lanes32::NW : Lanes64::NW;
+}
 
 cudaError_t launch_scan(const ScanArgs& args, int dtype, cudaStream_t s) {
     ScanArgs a = args;

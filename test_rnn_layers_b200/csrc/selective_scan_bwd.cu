@@ -18,8 +18,8 @@
 // one after the other and adds their shares of dB and dC up in registers: B and C are read and the shares
 // summed over the warp half as often (29.6 instead of 37.8 warp instructions a state and token), for 255
 // registers and two warps a scheduler.  Measured for 8 x 2048 tokens, 2048 channels, N = 16, bf16, gated:
-// 1.2 ms, 48 % of the issue slots used; one channel a lane at 128 registers and twice the warps takes
-// 5 % longer.  The sums over the block's warps go through shared memory, those over the blocks of a group
+// 1.0 ms; one channel a lane at 128 registers and twice the warps uses 71 % of the issue slots of a busy
+// SM and takes 4 % longer.  The sums over the block's warps go through shared memory, those over the blocks of a group
 // and over the sequences through a second kernel, all in a fixed order.
 //
 // Few long sequences are cut into spans as in the forward: a first launch finds what each span passes
@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(Y::THREADS) scan_bwd_kernel(const ScanBwdArgs 
                 for (int i = 0; i < S / 2; ++i)
                     av[t][i] = FULL || t < n ? decay2(mul2(dt, A2[m][i])) : both(1.f);
             }
+            __syncwarp();  // (here and below: the compiler moves no load across it, which saves it 30 spills a chunk)
             if constexpr (!SPAN) {
                 if constexpr (PAD) {
                     load_state<S, PAD>(ckpt + t0 / kT * hrow + hoff[m], left, h0);
@@ -294,6 +295,7 @@ __global__ void __launch_bounds__(Y::THREADS) scan_bwd_kernel(const ScanBwdArgs 
                     }
                 }
             }
+            __syncwarp();
             // back through it; the sums over a channel's lanes for P tokens at a time
             constexpr int G = P < kT ? P : kT;
             float y[G], s1[G], s2[G];
@@ -358,11 +360,14 @@ __global__ void __launch_bounds__(Y::THREADS) scan_bwd_kernel(const ScanBwdArgs 
         };
         if (n == kT) {
             channel(std::true_type{}, std::integral_constant<int, 0>{});
+            __syncwarp();
             if constexpr (R == 2) channel(std::true_type{}, std::integral_constant<int, R - 1>{});
         } else {
             channel(std::false_type{}, std::integral_constant<int, 0>{});
+            __syncwarp();
             if constexpr (R == 2) channel(std::false_type{}, std::integral_constant<int, R - 1>{});
         }
+        __syncwarp();
         if constexpr (!SPAN) {
             float share[2 * kT * S];  // [dB, dC][token][n]
 #pragma unroll
@@ -491,6 +496,10 @@ bool rows_on_16(const void* p, RowStride r, const ScanBwdArgs& a, size_t esz) {
 
 int scan_bwd_channels(int N) {
     return N <= 4 ? Lanes4::CH : N <= 8 ? Lanes8::CH : N <= 16 ? Lanes16::CH : N <= 32 ? Lanes32::CH : Lanes64::CH;
+}
+
+int scan_bwd_warps(int N) {
+    return N <= 4 ? Lanes4::NW : N <= 8 ? Lanes8::NW : N <= 16 ? Lanes16::NW : N <= 32 ? Lanes32::NW : Lanes64::NW;
 }
 
 cudaError_t launch_scan_bwd(const ScanBwdArgs& args, int dtype, cudaStream_t s) {

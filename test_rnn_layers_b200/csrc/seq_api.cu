@@ -21,6 +21,7 @@ constexpr long long kMaxTokens = 1ll << 30;
 constexpr long long kMaxChannels = 1ll << 24;
 constexpr int kMaxStates = 64;
 constexpr int kSms = 148;  // B200
+constexpr int kMinSpan = 32;  // tokens: 16 and 64 are slower or the same for 2 x 333 and 1 x 1000 tokens
 
 int check_shape(int n_seq, long long L, int dim, int dtype) {
     if (n_seq < 1 || n_seq > (1 << 24)) return fail(TTT_ERR_ARG, "n_seq must be in [1, 2^24] (got %d)", n_seq);
@@ -121,7 +122,7 @@ Split scan_split(int n_seq, long long L, long long longest, bool packed, int dim
     const long long tiles = static_cast<long long>(groups) * ((r + ch - 1) / ch);
     const int whole = static_cast<int>((L + 16) / 16 * 16);  // past every token
     Split s{false, whole, n_seq};
-    const long long blocks = tiles * n_seq, total = packed ? L : n_seq * L, slots = 2 * kSms;
+    const long long blocks = tiles * n_seq, total = packed ? L : n_seq * L, slots = kSms * (16 / ttt::scan_warps(N));
     const double t_whole = longest * (blocks <= kSms ? 0.11 : 0.17), t_split = 1.7 * total * tiles / 1720.0 + 10.0;
     if (blocks >= slots || t_split >= t_whole) return s;
     // two rounds of blocks, each full: 2 * slots blocks in all
@@ -130,7 +131,7 @@ Split scan_split(int n_seq, long long L, long long longest, bool packed, int dim
     long long spans = packed ? per_tile : per_tile / n_seq;
     if (spans < 1) spans = 1;
     long long span = ((packed ? total : L) + spans - 1) / spans;
-    span = ((span < 64 ? 64 : span) + 15) / 16 * 16;
+    span = ((span < kMinSpan ? kMinSpan : span) + 15) / 16 * 16;
     if (span * 2 > longest) return s;
     s.on = true;
     s.span = static_cast<int>(span);
@@ -142,14 +143,14 @@ size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 // The same for the backward, whose blocks hold up to 64 channels: spans where whole sequences would
 // leave most of the GPU idle.
-Split bwd_split(int n_seq, long long L, bool packed, long long tiles) {
+Split bwd_split(int n_seq, long long L, bool packed, long long tiles, int N) {
     Split s{false, static_cast<int>((L + 16) / 16 * 16), n_seq};
-    const long long blocks = tiles * n_seq, slots = 2 * kSms, total = packed ? L : n_seq * L;
+    const long long blocks = tiles * n_seq, slots = kSms * (8 / ttt::scan_bwd_warps(N)), total = packed ? L : n_seq * L;
     if (blocks * 2 > slots) return s;
     long long spans = packed ? slots / tiles - n_seq / 2 : slots / tiles / n_seq;
     if (spans < 1) spans = 1;
     long long span = ((packed ? total : L) + spans - 1) / spans;
-    span = ((span < 32 ? 32 : span) + 15) / 16 * 16;
+    span = ((span < kMinSpan ? kMinSpan : span) + 15) / 16 * 16;
     if (span * 2 > L) return s;
     s.on = true;
     s.span = static_cast<int>(span);
@@ -434,7 +435,7 @@ BwdLayout bwd_layout(int n_seq, long long L, bool packed, int dim, int groups, i
     BwdLayout y{};
     const int ch = ttt::scan_bwd_channels(N);
     y.tiles = (dim / groups + ch - 1) / ch;
-    y.split = bwd_split(n_seq, L, packed, static_cast<long long>(groups) * y.tiles);
+    y.split = bwd_split(n_seq, L, packed, static_cast<long long>(groups) * y.tiles, N);
     const size_t rows = static_cast<size_t>(packed ? L : n_seq * L), state = static_cast<size_t>(dim) * N * 4;
     const size_t slots = static_cast<size_t>(y.split.slots);
     y.part_a = up256(y.tiles * rows * groups * 2 * N * 4);

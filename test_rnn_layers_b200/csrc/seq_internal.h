@@ -138,6 +138,8 @@ int conv_bwd_span(int n_seq, long long L, bool packed, int D, int dtype);
 
 int scan_channels(int N);        // channels per block of the scan kernel
 int scan_bwd_channels(int N);    // and of its gradient's
+int scan_warps(int N);           // warps per block of the scan kernel (16 fit an SM)
+int scan_bwd_warps(int N);       // and of its gradient's (8 fit)
 cudaError_t launch_scan(const ScanArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_scan_step(const ScanStepArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_scan_bwd(const ScanBwdArgs& a, int dtype, cudaStream_t s);
