@@ -10,7 +10,7 @@
 //
 // What bounds it: a channel and token moves 4 elements (u, delta, z, out; 8 bytes in bf16) and takes
 // N exponentials, on a unit that does 16 a cycle and SM, next to 9 N multiplications (4 for 2^x near
-// zero).  Measured for 8 x 2048 tokens, 2048 channels, N = 16, bf16, gated: 348 us, where the bytes take
+// zero).  Measured for 8 x 2048 tokens, 2048 channels, N = 16, bf16, gated: 342 us, where the bytes take
 // 41; 13.1 warp instructions a state and token; on the SMs with two blocks 69 % of the issue slots are
 // used, the FMA pipe 55 % (a pair of floats takes it two cycles), the exponential unit 53 %, shared
 // memory 43 % of the time, with 3.5 warps a scheduler in all.
@@ -27,7 +27,7 @@
 // sum of dt; the second starts each span from the spans before it,
 //   h = exp(A sum dt) h + end state of the span,
 // and writes the outputs.  That is about 1.7 times the work, for as many times the blocks: one sequence of
-// 8200 tokens takes 291 us instead of 900.
+// 8200 tokens takes 287 us instead of 900.
 #include "seq_common.cuh"
 
 namespace ttt {
