@@ -546,7 +546,8 @@ int ttt_linear_backward_ckpt(const void* XQ, const void* XK, const void* XV, con
  *    scan's state are float32.  Sums, states and the gradients of the parameters are held in float32;
  *    results are rounded to dtype once.
  *  - The calls allocate nothing, wait for nothing on the device and may be captured into a graph.
- *    Results do not depend on timing.  Sizes: n_seq <= 2^24, L < 2^30, dim <= 2^24.
+ *    Results do not depend on timing.  Sizes: n_seq <= 2^24, L < 2^30, dim <= 2^22, and an operand's
+ *    rows within 2^50 elements.
  */
 
 /*
@@ -682,7 +683,8 @@ int ttt_selective_scan_backward(const void* u, const void* delta, const float* A
 /*
  * ttt_cache_copy -- page dst[i] = page src[i], i < n <= n_pages.  A pair is made (copied[i] = 1) if both
  * indexes are pages, they differ, dst[i] is not an earlier pair's destination and not any pair's
- * source; otherwise copied[i] = 0.  src, dst, copied: int32 [n].  workspace: int32 [1 + 2 n].
+ * source; otherwise copied[i] = 0.  n <= 16384 a call (TTT_ERR_UNSUPPORTED above).  src, dst, copied:
+ * int32 [n].  workspace: int32 [1 + 2 n].
  */
 int ttt_cache_copy(void* const* tensors, const long long* page_bytes, int n_tensors, int n_pages, const int* src,
                    const int* dst, int n, int* copied, int* workspace, void* stream);

@@ -1007,7 +1007,7 @@ def _i32(like, *sizes):
 def ttt_cache_copy(tensors, src, dst, stream=None):
     """Copy pages: page dst[i] of every tensor (each [n_pages, ...]) becomes page src[i].  Returns copied
     (int32 [n]): 0 where a pair was refused (an index outside the cache, a destination named before or
-    also named as a source)."""
+    also named as a source).  At most 16384 pairs a call."""
     return _cache_copy(src, tensors, dst, stream=stream)
 
 

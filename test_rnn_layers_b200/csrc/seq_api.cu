@@ -18,7 +18,9 @@ using ttt::SeqShape;
 using ttt::Span;
 
 constexpr long long kMaxTokens = 1ll << 30;
-constexpr long long kMaxChannels = 1ll << 24;
+constexpr long long kMaxChannels = 1ll << 22;  // of one channel a thread, 2^15 blocks of 128 in a grid's y
+constexpr long long kMaxElements = 1ll << 50;  // of an operand, first to last: sizes in bytes stay far inside 64 bits
+constexpr int kMaxCopies = 1 << 14;            // each copy by index is compared with all others of its call
 constexpr int kMaxStates = 64;
 constexpr int kSms = 148;  // B200
 constexpr int kMinSpan = 32;  // tokens: 16 and 64 are slower or the same for 2 x 333 and 1 x 1000 tokens
@@ -26,7 +28,7 @@ constexpr int kMinSpan = 32;  // tokens: 16 and 64 are slower or the same for 2 
 int check_shape(int n_seq, long long L, int dim, int dtype) {
     if (n_seq < 1 || n_seq > (1 << 24)) return fail(TTT_ERR_ARG, "n_seq must be in [1, 2^24] (got %d)", n_seq);
     if (L < 0 || L >= kMaxTokens) return fail(TTT_ERR_ARG, "L must be in [0, 2^30) (got %lld)", L);
-    if (dim < 1 || dim > kMaxChannels) return fail(TTT_ERR_ARG, "the channels must be in [1, 2^24] (got %d)", dim);
+    if (dim < 1 || dim > kMaxChannels) return fail(TTT_ERR_ARG, "the channels must be in [1, 2^22] (got %d)", dim);
     if (dtype != TTT_F32 && dtype != TTT_BF16) return fail(TTT_ERR_ARG, "dtype must be TTT_F32 or TTT_BF16");
     return TTT_OK;
 }
@@ -48,9 +50,9 @@ long long extent(RowStride r, bool packed, int n_seq, long long L, long long wid
 
 // Input rows may repeat (stride 0); an output's must not touch one another.
 int check_stride(const char* name, RowStride r, bool packed, int n_seq, long long L, long long width, bool output) {
-    const long long big = 1ll << 50;
-    if (r.t < 0 || r.t > big || (!packed && (r.b < 0 || r.b > big)))
-        return fail(TTT_ERR_ARG, "%s: strides must be in [0, 2^50] (got %lld, %lld)", name, r.b, r.t);
+    const long long steps_t = L > 1 ? L - 1 : 1, steps_b = n_seq > 1 ? n_seq - 1 : 1;
+    if (r.t < 0 || r.t > kMaxElements / steps_t || (!packed && (r.b < 0 || r.b > kMaxElements / steps_b)))
+        return fail(TTT_ERR_ARG, "%s: strides must be >= 0, the rows within 2^50 elements (got %lld, %lld)", name, r.b, r.t);
     if (!output || L == 0) return TTT_OK;
     const bool one_b = packed || n_seq == 1, one_t = L <= 1;
     bool apart = (one_t || r.t >= width) && (one_b || r.b >= width);
@@ -541,7 +543,8 @@ int check_tensors(void* const* tensors, const long long* page_bytes, int n_tenso
     long long all = 0;
     for (int i = 0; i < n_tensors; ++i) {
         if (!tensors[i]) return fail(TTT_ERR_ARG, "tensor %d is null", i);
-        if (page_bytes[i] < 1 || page_bytes[i] > (1ll << 40)) return fail(TTT_ERR_ARG, "page_bytes[%d] must be in [1, 2^40] (got %lld)", i, page_bytes[i]);
+        if (page_bytes[i] < 1 || page_bytes[i] > (1ll << 40) || page_bytes[i] > kMaxElements / n_pages)
+            return fail(TTT_ERR_ARG, "page_bytes[%d] must be in [1, 2^40], n_pages of them within 2^50 bytes (got %lld)", i, page_bytes[i]);
         t->base[i] = static_cast<char*>(tensors[i]);
         t->bytes[i] = page_bytes[i];
         all += page_bytes[i];
@@ -576,6 +579,7 @@ int ttt_cache_copy(void* const* tensors, const long long* page_bytes, int n_tens
     ttt::CacheTensors t;
     TTT_TRY(check_tensors(tensors, page_bytes, n_tensors, n_pages, &t));
     if (n < 0 || n > n_pages) return fail(TTT_ERR_ARG, "n must be in [0, n_pages] (got %d of %d)", n, n_pages);
+    if (n > kMaxCopies) return fail(TTT_ERR_UNSUPPORTED, "at most %d copies a call (got %d)", kMaxCopies, n);
     if (n == 0) return ok();
     TTT_TRY(need("src", src, 4));
     TTT_TRY(need("dst", dst, 4));

@@ -158,6 +158,29 @@ def test_cache_rejects(libttt, what, kw, code):
     assert cache(libttt.lib(), what, **kw) == code
 
 
+@pytest.mark.parametrize("kw", [
+    dict(D=(1 << 22) + 1, s=strides(0, 1 << 23, 1 << 40, 1 << 23)),  # more channels than a grid's second axis takes
+    dict(n=1 << 20, s=strides(1 << 44, 64, 2560, 64)),                # sizes that pass 64 bits on the host: the aliasing
+    dict(s=strides(0, 1 << 48, 2560, 64)),                            # check would be made on their remainders
+])
+def test_conv_refuses_sizes_past_its_arithmetic(libttt, kw):
+    assert conv(libttt.lib(), si=None, so=None, pages=None, **kw) == -1
+
+
+def test_scan_and_step_refuse_sizes_past_their_arithmetic(libttt):
+    wide = strides(*([0, 1 << 48] + [2560, 64] * 5))
+    assert scan(libttt.lib(), s=wide) == -1
+    assert conv_step(libttt.lib(), n=1 << 20, np=1 << 20, s=strides(1 << 44, 64)) == -1
+
+
+def test_cache_refuses_sizes_past_its_arithmetic(libttt):
+    lib = libttt.lib()
+    assert cache(lib, "copy", tensors=((A, 1 << 40),), n_pages=1 << 30) == -1
+    assert cache(lib, "compact", tensors=((A, 1 << 40),), n_pages=1 << 24) == -1
+    # every copy by index is compared with all others of its call
+    assert cache(lib, "copy", tensors=((1 << 40, 4),), n_pages=1 << 20, n=(1 << 14) + 1) == -6
+
+
 def test_nothing_to_do_is_fine(libttt):
     lib = libttt.lib()
     assert cache(lib, "copy", n=0, a=None, b=None) == 0
