@@ -215,9 +215,10 @@ __device__ __forceinline__ float silu_grad_f(float x, float sg) { return sg * fm
 // log1p(e) = 2 artanh(s) = s R(s^2); R is fitted to 4e-9 (least maximum of the relative error), so
 // the small steps e^x of a very negative x keep their relative accuracy.
 __device__ __forceinline__ float softplus_f(float x) {
-    // e^-|x|, the rounding of |x| log2(e) carried along
+    // e^-|x|, the rounding of |x| log2(e) carried along; 0 from where the product would pass the largest
+    // float (a mask of the type's lowest value) and long before
     const float m = -fabsf(x), y = m * kLog2e, y0 = fmaf(m, kLog2e, -y);
-    const float ey = ex2_approx(y), e = isinf(m) ? 0.0f : fmaf(ey, y0 * 0.6931471805599453f, ey);
+    const float ey = ex2_approx(y), e = m < -256.0f ? 0.0f : fmaf(ey, y0 * 0.6931471805599453f, ey);
     const float s = e * rcp_approx(2.0f + e), w = s * s;
     float r = fmaf(w, 0.2817833423614502f, 0.27960601449012756f);
     r = fmaf(w, r, 0.40024909377098083f);

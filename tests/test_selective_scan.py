@@ -254,6 +254,32 @@ def test_extreme_steps(libttt):
     assert torch.isnan(out[0, 7:, 4]).all() and torch.isfinite(out[0, :7]).all() and torch.isfinite(out[0, :, 5:]).all()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("mask", ["lowest", "-inf"])
+def test_masked_steps(libttt, dt, mask):
+    """Tokens switched off by their delta, the type's lowest value or -inf: softplus of it is 0, so the state
+    passes through them unchanged and their delta has no gradient."""
+    n_seq, L, D, N = 2, 37, 12, 16
+    s = inputs((n_seq, L), D, N, 1, DT[dt], 71)
+    off = torch.tensor([0, 5, 6, 16, 31, 32, 36], device="cuda")
+    s["delta"][:, off] = torch.finfo(DT[dt]).min if mask == "lowest" else -math.inf
+    s["delta"][1] = s["delta"][0, 0, 0]  # a sequence with nothing left
+    h0 = torch.randn(n_seq, D, N, generator=torch.Generator().manual_seed(5)).cuda()
+    want = want_of(s, n_seq, L, h0=h0)
+    a, k = positional(s)
+    end = h0.clone()
+    out = libttt.ttt_selective_scan_forward(*a, **k, state_in=end, state_out=end)
+    ref.check("out", out, want.out, want.out_mag, want.c, DT[dt])
+    ref.check("state", end, torch.stack(want.last), torch.stack(want.last_mag), want.c, torch.float32)
+    assert torch.equal(end[1], h0[1])
+    g, _ = check_grads(libttt, s, n_seq, L, DT[dt], h0=h0, dlast=h0.flip(0).contiguous())
+    assert (g["ddelta"][:, off] == 0).all() and (g["ddelta"][1] == 0).all()
+    pool, t = h0.clone(), {n_: v[:, 5] if n_ in ("u", "delta", "B", "C", "z") else v for n_, v in s.items()}
+    a, k = positional(t)
+    y = libttt.ttt_selective_scan_step(*a, pool, **k)
+    assert torch.equal(pool, h0) and torch.isfinite(y).all()
+
+
 def test_empty_sequences(libttt):
     s = inputs((2, 0), 8, 16, 1, torch.bfloat16, 51)
     a, k = positional(s)
