@@ -40,8 +40,10 @@ enum Mode { kSpanState, kOut, kOutGated };
 // The layouts, by the number of states N.  Four states a lane and one channel a lane for N = 16: two
 // channels a lane read B and C half as often but leave 1.7 warps for each scheduler at the sizes of a
 // training batch, eight states a lane likewise (8 x 2048 tokens, 2048 channels: 353 us against 389 and
-// 386 us; two states a lane 500 us; four warps a block instead of eight 382 us).
-using Lanes4 = Lanes<4, 1, 1, 2>;
+// 386 us; two states a lane 500 us; four warps a block instead of eight 382 us).  For N <= 4 two lanes a
+// channel, which share what is done once a channel and token (8 x 2048 tokens, 8192 channels: 540 us, and
+// 561 us with N = 3; one lane a channel 570 and 759 us).
+using Lanes4 = Lanes<2, 2, 1, 4>;
 using Lanes8 = Lanes<4, 2, 1, 4>;
 using Lanes16 = Lanes<4, 4, 1, 8>;
 using Lanes32 = Lanes<4, 8, 2, 8>;
