@@ -140,29 +140,11 @@ __global__ void __launch_bounds__(Y::THREADS) scan_kernel(const ScanArgs a) {
         chunk = a.s.cu ? slot_base(a.s.cu, p.b, a.s.L, kScanChunk)
                        : p.b * ((a.s.L + kScanChunk - 1) / kScanChunk);
 
-    // One 16-byte piece of a tile's row: asynchronously where it lies on a 16-byte boundary.
-    auto fetch = [&](T* to, const T* from, bool wide, int ch) {
-        if (wide) {
-            cp_async_16(to, from);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VE; ++i)
-                if (c0 + ch + i < r) to[i] = from[i];
-        }
-    };
     auto store_out = [&](int buf, int t0) {          // the tile's outputs, left where u was
         for (int e = threadIdx.x; e < PIECES; e += TH) {
             const int t = e / (CH / VE), ch = e % (CH / VE) * VE;
             if (t0 + t < last) {
-                const T* from = &raw[buf][0][t][ch];
-                T* to = out + (t0 + t) * a.so.t + ch;
-                if (a.wide & 8 && c0 + ch + VE <= r) {
-                    *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < VE; ++i)
-                        if (c0 + ch + i < r) to[i] = from[i];
-                }
+                store_piece(out + (t0 + t) * a.so.t + ch, &raw[buf][0][t][ch], a.wide & 8, r - c0 - ch);
             }
         }
     };
@@ -170,10 +152,10 @@ __global__ void __launch_bounds__(Y::THREADS) scan_kernel(const ScanArgs a) {
         for (int e = threadIdx.x; e < PIECES; e += TH) {
             const int t = e / (CH / VE), ch = e % (CH / VE) * VE;
             if (t0 + t < last) {
-                const bool in = c0 + ch + VE <= r;
-                fetch(&raw[buf][0][t][ch], u + (t0 + t) * a.su.t + ch, in && (a.wide & 1), ch);
-                fetch(&raw[buf][1][t][ch], dl + (t0 + t) * a.sdt.t + ch, in && (a.wide & 2), ch);
-                if (GATE) fetch(&raw[buf][GATE ? 2 : 0][t][ch], z + (t0 + t) * a.sz.t + ch, in && (a.wide & 4), ch);
+                const int n = r - c0 - ch;
+                fetch_piece(&raw[buf][0][t][ch], u + (t0 + t) * a.su.t + ch, a.wide & 1, n);
+                fetch_piece(&raw[buf][1][t][ch], dl + (t0 + t) * a.sdt.t + ch, a.wide & 2, n);
+                if (GATE) fetch_piece(&raw[buf][GATE ? 2 : 0][t][ch], z + (t0 + t) * a.sz.t + ch, a.wide & 4, n);
             }
         }
     };

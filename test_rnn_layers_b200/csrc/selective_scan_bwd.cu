@@ -145,24 +145,29 @@ __global__ void __launch_bounds__(Y::THREADS) scan_bwd_kernel(const ScanBwdArgs 
     const float* ckpt = a.ckpt + chunk0 * hrow;
 
     T rbc[NB];
-    auto fetch = [&](T* to, const T* from, bool wide, int ch) {
-        if (wide) {
-            cp_async_16(to, from);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VE; ++i)
-                if (c0 + ch + i < r) to[i] = from[i];
-        }
-    };
     auto load_chunk = [&](int buf, int t0) {
         for (int e = threadIdx.x; e < PIECES; e += TH) {
             const int t = e / (CH / VE), ch = e % (CH / VE) * VE;
             if (t0 + t < last) {
-                const bool in = c0 + ch + VE <= r;
-                if (!SPAN) fetch(&raw[buf][0][t][ch], u + (t0 + t) * a.su.t + ch, in && (a.wide & 1), ch);
-                fetch(&raw[buf][1][t][ch], dl + (t0 + t) * a.sdt.t + ch, in && (a.wide & 2), ch);
-                fetch(&raw[buf][2][t][ch], dout + (t0 + t) * a.sdo.t + ch, in && (a.wide & 8), ch);
-                if (GATE) fetch(&raw[buf][GATE ? 3 : 0][t][ch], z + (t0 + t) * a.sz.t + ch, in && (a.wide & 4), ch);
+                const int n = r - c0 - ch;
+                const T *pu = u + (t0 + t) * a.su.t + ch, *pd = dl + (t0 + t) * a.sdt.t + ch, *po = dout + (t0 + t) * a.sdo.t + ch,
+                        *pz = GATE ? z + (t0 + t) * a.sz.t + ch : nullptr;
+                if (n >= VE && (a.wide & 1)) {
+                    if (!SPAN) cp_async_16(&raw[buf][0][t][ch], pu);
+                    cp_async_16(&raw[buf][1][t][ch], pd);
+                    cp_async_16(&raw[buf][2][t][ch], po);
+                    if (GATE) cp_async_16(&raw[buf][GATE ? 3 : 0][t][ch], pz);
+                } else if (a.wide & 2) {  // 8 x 2048 tokens of 2052 channels, a training step: 1662 us, by elements 2255
+                    if (!SPAN) fetch_words(&raw[buf][0][t][ch], pu, n);
+                    fetch_words(&raw[buf][1][t][ch], pd, n);
+                    fetch_words(&raw[buf][2][t][ch], po, n);
+                    if (GATE) fetch_words(&raw[buf][GATE ? 3 : 0][t][ch], pz, n);
+                } else {  // (words for every other row of an odd length are slower than no words)
+                    if (!SPAN) copy_elements(&raw[buf][0][t][ch], pu, n);
+                    copy_elements(&raw[buf][1][t][ch], pd, n);
+                    copy_elements(&raw[buf][2][t][ch], po, n);
+                    if (GATE) copy_elements(&raw[buf][GATE ? 3 : 0][t][ch], pz, n);
+                }
             }
         }
         if constexpr (!SPAN && !PAD) {
@@ -487,9 +492,9 @@ cudaError_t dispatch(const ScanBwdArgs& a, cudaStream_t s) {
     return pick<T, Lanes64>(a, s);
 }
 
-bool rows_on_16(const void* p, RowStride r, const ScanBwdArgs& a, size_t esz) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (a.s.cu || r.b * esz % 16 == 0) && r.t * esz % 16 == 0 &&
-           (a.groups == 1 || a.dim / a.groups * esz % 16 == 0);
+bool rows_on(size_t bytes, const void* p, RowStride r, const ScanBwdArgs& a, size_t esz) {
+    return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (a.s.cu || r.b * esz % bytes == 0) && r.t * esz % bytes == 0 &&
+           (a.groups == 1 || a.dim / a.groups * esz % bytes == 0);
 }
 
 }  // namespace
@@ -506,10 +511,12 @@ cudaError_t launch_scan_bwd(const ScanBwdArgs& args, int dtype, cudaStream_t s) 
     ScanBwdArgs a = args;
     const size_t esz = dtype == 0 ? 4 : 2;
     const RowStride own{a.s.L * a.dim, a.dim};
-    a.wide = (rows_on_16(a.u, a.su, a, esz) ? 1 : 0) | (rows_on_16(a.delta, a.sdt, a, esz) ? 2 : 0) |
-             (a.z && rows_on_16(a.z, a.sz, a, esz) ? 4 : 0) | (rows_on_16(a.d_out, a.sdo, a, esz) ? 8 : 0) |
-             (rows_on_16(a.du, own, a, esz) ? 16 : 0) | (rows_on_16(a.ddelta, own, a, esz) ? 32 : 0) |
-             (a.dz && rows_on_16(a.dz, own, a, esz) ? 64 : 0);
+    auto inputs_on = [&](size_t n) {
+        return rows_on(n, a.u, a.su, a, esz) && rows_on(n, a.delta, a.sdt, a, esz) && (!a.z || rows_on(n, a.z, a.sz, a, esz)) &&
+               rows_on(n, a.d_out, a.sdo, a, esz);
+    };
+    a.wide = (inputs_on(16) ? 1 : 0) | (inputs_on(4) ? 2 : 0) | (rows_on(16, a.du, own, a, esz) ? 16 : 0) |
+             (rows_on(16, a.ddelta, own, a, esz) ? 32 : 0) | (a.dz && rows_on(16, a.dz, own, a, esz) ? 64 : 0);
     return dtype == 0 ? dispatch<float>(a, s) : dispatch<__nv_bfloat16>(a, s);
 }
 

@@ -312,4 +312,44 @@ __device__ __forceinline__ void cp_async_16(void* smem, const void* gmem) {
 }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// Pieces of 16 bytes between rows and shared memory, of which `n` elements are there.  Rows on 4-byte
+// boundaries go by words, to shared memory asynchronously: plain loads would be waited for (the scan of
+// 8 x 2048 tokens, 2052 channels in bf16: 387 us, by elements 577).
+template <typename T>
+__device__ __forceinline__ void copy_elements(T* to, const T* from, int n) {
+#pragma unroll
+    for (int i = 0; i < 16 / static_cast<int>(sizeof(T)); ++i)
+        if (i < n) to[i] = from[i];
+}
+template <typename T>
+__device__ __forceinline__ void fetch_words(T* to, const T* from, int n) {
+    constexpr int VE = 16 / sizeof(T), E = 4 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < VE; i += E) {
+        if (i + E <= n) cp_async_4(to + i, from + i);
+        else if (i < n) to[i] = from[i];
+    }
+}
+template <typename T>
+__device__ __forceinline__ void fetch_piece(T* to, const T* from, bool wide, int n) {
+    if (wide && n >= 16 / static_cast<int>(sizeof(T))) cp_async_16(to, from);
+    else if (reinterpret_cast<uintptr_t>(from) % 4 == 0) fetch_words(to, from, n);
+    else copy_elements(to, from, n);
+}
+template <typename T>
+__device__ __forceinline__ void store_piece(T* to, const T* from, bool wide, int n) {
+    constexpr int VE = 16 / sizeof(T), E = 4 / sizeof(T);
+    if (wide && n >= VE) {
+        *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+    } else if (reinterpret_cast<uintptr_t>(to) % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < VE; i += E) {
+            if (i + E <= n) *reinterpret_cast<uint32_t*>(to + i) = *reinterpret_cast<const uint32_t*>(from + i);
+            else if (i < n) to[i] = from[i];
+        }
+    } else {
+        copy_elements(to, from, n);
+    }
+}
+
 }  // namespace ttt

@@ -110,7 +110,8 @@ struct ScanBwdArgs {
     float* part_d;               // [n_slots][2][dim]: d D, d bias
     float* seg_dh;               // [n_slots][dim][N]: what each span passes back, from nothing behind it
     float* seg_dt;               // [n_slots][dim]: each span's sum of dt
-    int wide;                    // bits: the rows of u, delta, z, d_out, du, d delta, dz start on 16-byte boundaries
+    int wide;                    // bits 0, 1: the rows of u, delta, z, d_out start on 16-byte, 4-byte boundaries;
+                                 // bits 4 .. 6: those of du, d delta, dz on 16-byte boundaries
 };
 
 constexpr int kCacheMaxTensors = 512;
